@@ -91,7 +91,12 @@ typedef enum {
 
 typedef enum { SVDQ_NVFP4 = 0, SVDQ_INT4 = 1 } svdq_format;
 
-typedef enum { SVDQ_EPI_NONE = 0, SVDQ_EPI_GELU_TANH = 1 } svdq_epilogue;
+/* SVDQ_EPI_SILU: the 16-bit calls (svdq_dense_linear, svdq_gated_linear and
+ * their backward passes) only. */
+typedef enum { SVDQ_EPI_NONE = 0, SVDQ_EPI_GELU_TANH = 1, SVDQ_EPI_SILU = 2 } svdq_epilogue;
+
+/* Element types of the 16-bit calls and of the layer norm. */
+typedef enum { SVDQ_BF16 = 0, SVDQ_FP16 = 1, SVDQ_FP32 = 2 } svdq_dtype;
 
 /* Opaque, library-owned prepared weights of one layer. */
 typedef struct svdq_weights svdq_weights;
@@ -497,6 +502,83 @@ svdq_status svdq_awq_linear(const svdq_awq_weights* w, int M, const void* X, voi
  *   SHAPE, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
  * ------------------------------------------------------------------------ */
 svdq_status svdq_awq_gemm(const svdq_awq_weights* w, int M, const void* X, void* Y, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The layers around the 4-bit ones, in 16 bits, forward and backward: the
+ * projections a quantizer leaves dense, the gated feed-forward, the layer
+ * norm in front of them.
+ *
+ * Conventions of these calls
+ *   - dt: SVDQ_BF16 or SVDQ_FP16 (layer norm: also SVDQ_FP32); every tensor
+ *     of a call has that type except mean and rstd (float32).  Sums are
+ *     float32; every output is rounded once from float32.  A backward pass
+ *     also rounds dZ (dG, dU) to dt, the operand type of its products.
+ *   - Activations (X, Y, residual, H, dY, dH, dX) are rows with a stride ld in
+ *     elements, ld >= the row's length, ld % 8 == 0 (layer norm: any).
+ *     Weights, biases, kept pre-activations (Z, G, U) and weight gradients are
+ *     packed.
+ *   - K, N, F > 0 and multiples of 8, M >= 0.  M == 0: a forward call is a
+ *     no-op, a backward call writes zero weight and bias gradients.
+ *   - Device pointers 16-byte aligned (layer norm: to their element).
+ *   - Outputs overlap neither inputs nor each other, with one exception: Y
+ *     may be the residual itself (same pointer, same stride).
+ *   - The same inputs give the same bits on every run; the calls keep nothing
+ *     between calls and may be captured into CUDA graphs.  Calls that can
+ *     overlap on the GPU need workspaces of their own.
+ *   Errors of all of them: INVALID_ARG (null, unknown enum, bad scalar),
+ *   SHAPE (sizes and strides; a stride of 2^40 bytes or more), ALIGNMENT,
+ *   WORKSPACE, UNSUPPORTED_DEVICE, CUDA.
+ *
+ * svdq_dense_linear: z = X W + b (float32);  Y = act(z) + residual.
+ *   X [M][K], W_t [N][K] (nn.Linear order), bias [N] or NULL, residual [M][N]
+ *   or NULL, Y [M][N]; Z [M][N] or NULL receives z for the backward pass.
+ * svdq_dense_linear_backward: dz = dY act'(Z);  dX = dz W^T, dW[n][k] =
+ *   sum_m dz[m][n] X[m][k], dbias = sum_m dz (the residual's gradient is dY).
+ *   Z is read when act is not NONE.  dX, dW and dbias may each be NULL (then
+ *   W_t is not read without dX, X not without dW).
+ *   Workspace: svdq_dense_linear_backward_workspace_bytes.
+ * svdq_gated_linear: g = X Wg + bg, u = X Wu + bu;  H = act(g) u, both
+ *   products in one kernel that reads X once.  Wg_t, Wu_t [F][K], biases [F]
+ *   or NULL, H [M][F]; G and U [M][F] or NULL receive g and u.
+ * svdq_gated_linear_backward: dg = dH u act'(g), du = dH act(g);
+ *   dX = dg Wg^T + du Wu^T; dWg, dWu, dbias_g, dbias_u as above.  dX, the two
+ *   weight gradients (both or neither) and the two bias gradients (both or
+ *   neither) may be NULL.
+ *   Workspace: svdq_gated_linear_backward_workspace_bytes.
+ * svdq_layernorm: per row, mean and rstd = 1 / sqrt(var + eps) (biased
+ *   variance, two passes over the row), Y = (X - mean) rstd gamma + beta.
+ *   C >= 1; gamma and beta [C] (both or neither NULL); mean, rstd float32 [M]
+ *   or NULL; eps >= 0 and finite.  Y may be X itself (same pointer, same stride).
+ * svdq_layernorm_backward: with xh = (X - mean) rstd and g = dY gamma,
+ *   dX = rstd (g - mean(g) - xh mean(g xh)); dgamma = sum_m dY xh,
+ *   dbeta = sum_m dY (both or neither NULL; they may be asked for when gamma
+ *   is NULL).  dX may be NULL.  Workspace: svdq_layernorm_backward_workspace_bytes.
+ * ------------------------------------------------------------------------ */
+svdq_status svdq_dense_linear(svdq_dtype dt, int M, int K, int N, const void* X, long long ldx, const void* W_t,
+                              const void* bias, svdq_epilogue act, const void* residual, long long ldr, void* Y,
+                              long long ldy, void* Z, cudaStream_t stream);
+size_t svdq_dense_linear_backward_workspace_bytes(int M, int K, int N, svdq_epilogue act);
+svdq_status svdq_dense_linear_backward(svdq_dtype dt, int M, int K, int N, const void* dY, long long lddy,
+                                       const void* X, long long ldx, const void* W_t, const void* Z,
+                                       svdq_epilogue act, void* dX, long long lddx, void* dW, void* dbias,
+                                       void* workspace, size_t ws_bytes, cudaStream_t stream);
+svdq_status svdq_gated_linear(svdq_dtype dt, int M, int K, int F, const void* X, long long ldx, const void* Wg_t,
+                              const void* Wu_t, const void* bias_g, const void* bias_u, svdq_epilogue act, void* H,
+                              long long ldh, void* G, void* U, cudaStream_t stream);
+size_t svdq_gated_linear_backward_workspace_bytes(int M, int K, int F);
+svdq_status svdq_gated_linear_backward(svdq_dtype dt, int M, int K, int F, const void* dH, long long lddh,
+                                       const void* X, long long ldx, const void* Wg_t, const void* Wu_t,
+                                       const void* G, const void* U, svdq_epilogue act, void* dX, long long lddx,
+                                       void* dWg, void* dWu, void* dbias_g, void* dbias_u, void* workspace,
+                                       size_t ws_bytes, cudaStream_t stream);
+svdq_status svdq_layernorm(svdq_dtype dt, int M, int C, const void* X, long long ldx, const void* gamma,
+                           const void* beta, float eps, void* Y, long long ldy, float* mean, float* rstd,
+                           cudaStream_t stream);
+size_t svdq_layernorm_backward_workspace_bytes(int M, int C);
+svdq_status svdq_layernorm_backward(svdq_dtype dt, int M, int C, const void* dY, long long lddy, const void* X,
+                                    long long ldx, const void* gamma, const float* mean, const float* rstd, void* dX,
+                                    long long lddx, void* dgamma, void* dbeta, void* workspace, size_t ws_bytes,
+                                    cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Diagnostics.

@@ -26,7 +26,9 @@ if not os.path.exists(LIB_PATH):
 lib = ctypes.CDLL(LIB_PATH)
 
 SVDQ_NVFP4, SVDQ_INT4 = 0, 1
-SVDQ_EPI_NONE, SVDQ_EPI_GELU_TANH = 0, 1
+SVDQ_EPI_NONE, SVDQ_EPI_GELU_TANH, SVDQ_EPI_SILU = 0, 1, 2
+SVDQ_BF16, SVDQ_FP16, SVDQ_FP32 = 0, 1, 2
+DTYPES = {torch.bfloat16: SVDQ_BF16, torch.float16: SVDQ_FP16, torch.float32: SVDQ_FP32}
 STATUS = {0: "SVDQ_OK", 1: "SVDQ_ERR_INVALID_ARG", 2: "SVDQ_ERR_SHAPE", 3: "SVDQ_ERR_ALIGNMENT",
           4: "SVDQ_ERR_UNSUPPORTED_DEVICE", 5: "SVDQ_ERR_WORKSPACE", 6: "SVDQ_ERR_CUDA",
           7: "SVDQ_ERR_TIMEOUT", 8: "SVDQ_ERR_DEVICE_FAULT", 9: "SVDQ_ERR_NO_MEMORY"}
@@ -55,7 +57,7 @@ class AwqInfo(ctypes.Structure):
                 ("bias", ctypes.c_void_p)]
 
 
-_vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_vp, _i, _f, _sz, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
 _SIGS = {
     "svdq_status_string": (ctypes.c_char_p, [_i]),
     "svdq_calibrate_workspace_bytes": (_sz, [_i]),
@@ -89,6 +91,17 @@ _SIGS = {
     "svdq_awq_gemm": (_i, [_vp, _i, _vp, _vp, _vp]),
     "svdq_linear_host_workspace_bytes": (ctypes.c_size_t, [_vp, _i]),
     "svdq_linear_host": (_i, [_vp, _i, _vp, _i, _vp, _vp, ctypes.c_size_t, _vp]),
+    "svdq_dense_linear": (_i, [_i, _i, _i, _i, _vp, _ll, _vp, _vp, _i, _vp, _ll, _vp, _ll, _vp, _vp]),
+    "svdq_dense_linear_backward_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "svdq_dense_linear_backward": (_i, [_i, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _vp, _i, _vp, _ll, _vp, _vp, _vp,
+                                        _sz, _vp]),
+    "svdq_gated_linear": (_i, [_i, _i, _i, _i, _vp, _ll, _vp, _vp, _vp, _vp, _i, _vp, _ll, _vp, _vp, _vp]),
+    "svdq_gated_linear_backward_workspace_bytes": (_sz, [_i, _i, _i]),
+    "svdq_gated_linear_backward": (_i, [_i, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _i, _vp, _ll, _vp, _vp,
+                                        _vp, _vp, _vp, _sz, _vp]),
+    "svdq_layernorm": (_i, [_i, _i, _i, _vp, _ll, _vp, _vp, _f, _vp, _ll, _vp, _vp, _vp]),
+    "svdq_layernorm_backward_workspace_bytes": (_sz, [_i, _i]),
+    "svdq_layernorm_backward": (_i, [_i, _i, _i, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _ll, _vp, _vp, _vp, _sz, _vp]),
     "svdq_poll_device_error": (_i, [_vp]),
     "svdq_selftest_wait_timeout": (_i, [ctypes.c_uint, _vp]),
     "svdq_debug_override_cc": (None, [_i, _i]),
@@ -312,6 +325,129 @@ def svdq_awq_linear(w, M, X, Y, stream=None):
 
 def svdq_awq_gemm(w, M, X, Y, stream=None):
     _check(lib.svdq_awq_gemm(w, M, _ptr(X), _ptr(Y), _stream(stream)), "svdq_awq_gemm")
+
+
+# ------------------------------------------------------------------ 16-bit layers
+# The element type and the row strides the C calls take come from the tensors;
+# every tensor has to have the stated shape, X's (or dY's) type, and to lie on
+# the current device.
+def _rows(t, rows, cols, dt, dev, what):
+    """(address, row stride) of an activation: a [>= rows][cols] tensor whose
+    rows are contiguous."""
+    if t is None:
+        return None, 0
+    st, sh = t.stride(), t.shape
+    if t.dtype is not dt or t.get_device() != dev or len(sh) != 2 or sh[1] != cols or sh[0] < rows or \
+            (cols > 1 and st[1] != 1):
+        raise ValueError("svdq: %s has to be a %s tensor [%d][%d] with contiguous rows on the current device, not %s %s "
+                         "on %s" % (what, dt, rows, cols, t.dtype, tuple(sh), t.device))
+    return t.data_ptr(), (st[0] if rows > 1 else cols)   # the stride of a single row is never used
+
+
+def _flat(t, n, dt, dev, what):
+    """Address of a packed tensor of n elements."""
+    if t is None:
+        return None
+    if t.dtype is not dt or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        raise ValueError("svdq: %s has to be a packed %s tensor of %d elements on the current device, not %s %s on %s"
+                         % (what, dt, n, t.dtype, tuple(t.shape), t.device))
+    return t.data_ptr()
+
+
+def _workspace(t, ws_bytes, dev):
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("svdq: the workspace has to be packed memory of the current device")
+    return t.data_ptr(), t.numel() * t.element_size() if ws_bytes is None else ws_bytes
+
+
+def _type_of(t, what):
+    if t is None or t.dtype not in DTYPES:
+        raise ValueError("svdq: %s has to be a bfloat16, float16 or float32 tensor" % what)
+    return t.dtype, DTYPES[t.dtype], torch.cuda.current_device() if t.is_cuda else -2
+
+
+def svdq_dense_linear(M, K, N, X, W_t, bias, act, residual, Y, Z=None, stream=None):
+    dt, code, dev = _type_of(X, "X")
+    x, ldx = _rows(X, M, K, dt, dev, "X")
+    r, ldr = _rows(residual, M, N, dt, dev, "residual")
+    y, ldy = _rows(Y, M, N, dt, dev, "Y")
+    _check(lib.svdq_dense_linear(code, M, K, N, x, ldx, _flat(W_t, N * K, dt, dev, "W_t"),
+                                 _flat(bias, N, dt, dev, "bias"), act, r, ldr, y, ldy,
+                                 _flat(Z, M * N, dt, dev, "Z"), _stream(stream)), "svdq_dense_linear")
+
+
+def svdq_dense_linear_backward_workspace_bytes(M, K, N, act) -> int:
+    return lib.svdq_dense_linear_backward_workspace_bytes(M, K, N, act)
+
+
+def svdq_dense_linear_backward(M, K, N, dY, X, W_t, Z, act, dX, dW, dbias, workspace, ws_bytes=None, stream=None):
+    dt, code, dev = _type_of(dY, "dY")
+    dy, lddy = _rows(dY, M, N, dt, dev, "dY")
+    x, ldx = _rows(X, M, K, dt, dev, "X")
+    dx, lddx = _rows(dX, M, K, dt, dev, "dX")
+    ws, ws_bytes = _workspace(workspace, ws_bytes, dev)
+    _check(lib.svdq_dense_linear_backward(code, M, K, N, dy, lddy, x, ldx, _flat(W_t, N * K, dt, dev, "W_t"),
+                                          _flat(Z, M * N, dt, dev, "Z"), act, dx, lddx,
+                                          _flat(dW, N * K, dt, dev, "dW"), _flat(dbias, N, dt, dev, "dbias"), ws,
+                                          ws_bytes, _stream(stream)), "svdq_dense_linear_backward")
+
+
+def svdq_gated_linear(M, K, F, X, Wg_t, Wu_t, bias_g, bias_u, act, H, G=None, U=None, stream=None):
+    dt, code, dev = _type_of(X, "X")
+    x, ldx = _rows(X, M, K, dt, dev, "X")
+    h, ldh = _rows(H, M, F, dt, dev, "H")
+    _check(lib.svdq_gated_linear(code, M, K, F, x, ldx, _flat(Wg_t, F * K, dt, dev, "Wg_t"),
+                                 _flat(Wu_t, F * K, dt, dev, "Wu_t"), _flat(bias_g, F, dt, dev, "bias_g"),
+                                 _flat(bias_u, F, dt, dev, "bias_u"), act, h, ldh, _flat(G, M * F, dt, dev, "G"),
+                                 _flat(U, M * F, dt, dev, "U"), _stream(stream)), "svdq_gated_linear")
+
+
+def svdq_gated_linear_backward_workspace_bytes(M, K, F) -> int:
+    return lib.svdq_gated_linear_backward_workspace_bytes(M, K, F)
+
+
+def svdq_gated_linear_backward(M, K, F, dH, X, Wg_t, Wu_t, G, U, act, dX, dWg, dWu, dbias_g, dbias_u, workspace,
+                               ws_bytes=None, stream=None):
+    dt, code, dev = _type_of(dH, "dH")
+    dh, lddh = _rows(dH, M, F, dt, dev, "dH")
+    x, ldx = _rows(X, M, K, dt, dev, "X")
+    dx, lddx = _rows(dX, M, K, dt, dev, "dX")
+    ws, ws_bytes = _workspace(workspace, ws_bytes, dev)
+    _check(lib.svdq_gated_linear_backward(code, M, K, F, dh, lddh, x, ldx, _flat(Wg_t, F * K, dt, dev, "Wg_t"),
+                                          _flat(Wu_t, F * K, dt, dev, "Wu_t"), _flat(G, M * F, dt, dev, "G"),
+                                          _flat(U, M * F, dt, dev, "U"), act, dx, lddx,
+                                          _flat(dWg, F * K, dt, dev, "dWg"), _flat(dWu, F * K, dt, dev, "dWu"),
+                                          _flat(dbias_g, F, dt, dev, "dbias_g"),
+                                          _flat(dbias_u, F, dt, dev, "dbias_u"), ws, ws_bytes, _stream(stream)),
+           "svdq_gated_linear_backward")
+
+
+def svdq_layernorm(M, C, X, gamma, beta, eps, Y, mean=None, rstd=None, stream=None):
+    dt, code, dev = _type_of(X, "X")
+    x, ldx = _rows(X, M, C, dt, dev, "X")
+    y, ldy = _rows(Y, M, C, dt, dev, "Y")
+    _check(lib.svdq_layernorm(code, M, C, x, ldx, _flat(gamma, C, dt, dev, "gamma"), _flat(beta, C, dt, dev, "beta"),
+                              eps, y, ldy, _flat(mean, M, torch.float32, dev, "mean"),
+                              _flat(rstd, M, torch.float32, dev, "rstd"), _stream(stream)), "svdq_layernorm")
+
+
+def svdq_layernorm_backward_workspace_bytes(M, C) -> int:
+    return lib.svdq_layernorm_backward_workspace_bytes(M, C)
+
+
+def svdq_layernorm_backward(M, C, dY, X, gamma, mean, rstd, dX, dgamma, dbeta, workspace, ws_bytes=None, stream=None):
+    dt, code, dev = _type_of(dY, "dY")
+    dy, lddy = _rows(dY, M, C, dt, dev, "dY")
+    x, ldx = _rows(X, M, C, dt, dev, "X")
+    dx, lddx = _rows(dX, M, C, dt, dev, "dX")
+    ws, ws_bytes = _workspace(workspace, ws_bytes, dev)
+    _check(lib.svdq_layernorm_backward(code, M, C, dy, lddy, x, ldx, _flat(gamma, C, dt, dev, "gamma"),
+                                       _flat(mean, M, torch.float32, dev, "mean"),
+                                       _flat(rstd, M, torch.float32, dev, "rstd"), dx, lddx,
+                                       _flat(dgamma, C, dt, dev, "dgamma"), _flat(dbeta, C, dt, dev, "dbeta"), ws,
+                                       ws_bytes, _stream(stream)), "svdq_layernorm_backward")
 
 
 def svdq_poll_device_error(stream=None) -> int:

@@ -211,6 +211,22 @@ svdq_status svdq::handle_device_status(const svdq_weights* w) {
   return check_handle_device(w, &d);
 }
 
+svdq_status svdq::current_device_info(DeviceInfo* info) {
+  DevState* d = nullptr;
+  const svdq_status s = current_device(&d);
+  if (s != SVDQ_OK) return s;
+  info->num_sms = d->num_sms;
+  info->err = dev_err(d);
+  return SVDQ_OK;
+}
+
+bool svdq::encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inner,
+                                uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows) {
+  return tmap_2d(m, dt, ptr, inner, rows, row_bytes, box_inner, box_rows);
+}
+
+svdq_status svdq::cuda_status(cudaError_t e) { return from_cuda(e); }
+
 namespace {
 
 // Per-call NVFP4 activation tensor scale: where the amax slots are and where

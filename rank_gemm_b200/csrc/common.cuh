@@ -407,6 +407,36 @@ __device__ __forceinline__ float gelu_tanh(float y) {
   return y * r;
 }
 
+// SiLU, y / (1 + e^-y), with the same two approximations (relative error near
+// 1e-6 for a 16-bit output).
+__device__ __forceinline__ float sigmoid_approx(float y) {
+  float t, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(-1.4426950408889634f * y));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+  return r;
+}
+__device__ __forceinline__ float silu(float y) { return y * sigmoid_approx(y); }
+
+// (act(z), act'(z)) of an svdq_epilogue.  Both activations are z s(w) with s
+// the logistic function (silu: w = z; tanh-form GELU: w = 2u, u = sqrt(2/pi)
+// (z + 0.044715 z^3)), so act' = s + z s (1 - s) w'.  Where s (1 - s) is 0 the
+// second term is left out: w' may have overflowed there.
+__device__ __forceinline__ void act_and_slope(float z, int act, float& f, float& slope) {
+  if (act == 0) {
+    f = z;
+    slope = 1.f;
+    return;
+  }
+  const bool gelu = act == 1;
+  constexpr float k2 = 1.5957691216057308f;   // 2 sqrt(2/pi)
+  const float zz = z * z;
+  const float w = gelu ? k2 * z * fmaf(0.044715f, zz, 1.0f) : z;
+  const float dw = gelu ? k2 * fmaf(0.134145f, zz, 1.0f) : 1.0f;
+  const float s = sigmoid_approx(w), q = s * (1.0f - s);
+  f = z * s;
+  slope = q > 0.f ? fmaf(z * q, dw, s) : s;
+}
+
 // ----------------------------------------------------------------- 4-bit group quantizers
 // NVFP4, one 16-element group: a = max|v|; sb = E4M3(a / six_st) with six_st
 // = fl32(6 s_t); d = fl32(f32(sb) s_t); inv = fl32(1/d) (0 if d == 0);

@@ -22,6 +22,22 @@ cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes);
 // and holds the handle `w`; the status any entry point would return otherwise.
 svdq_status handle_device_status(const svdq_weights* w);
 
+// The current device's SM count and error word, with the status any entry
+// point returns when the device is not supported.
+struct DeviceInfo {
+  int num_sms;
+  DeviceErr err;
+};
+svdq_status current_device_info(DeviceInfo* info);
+
+// 2-D tensor map over row-major [rows][inner], 128-byte swizzled boxes; false
+// when the driver refuses it.
+bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t rows,
+                          uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows);
+
+// A CUDA status as an entry point returns it (clears a non-sticky error).
+svdq_status cuda_status(cudaError_t e);
+
 // ---------------------------------------------------------------- kernel 1
 struct K1Params {
   int M, K, K_pad, r_tot, r_pad;
@@ -221,5 +237,78 @@ cudaError_t launch_awq_gemv(const CUtensorMap& tmCode, const CUtensorMap& tmScal
                            AwqParams p, int num_sms, cudaStream_t stream);
 int awq_rows_per_block(int K, int M);
 size_t awq_smem_bytes(int K, int mb);
+
+// ---------------------------------------------------------------- 16-bit matrix products (gemm16.cu)
+// What is multiplied.  NT: both operands with the reduction index innermost
+// (X W^T).  NN: B with it outermost (dZ W).  TN: both outermost (dZ^T X).
+// GATED: NT with two weights and the gated epilogue.
+enum Gemm16Op { GEMM16_NT, GEMM16_GATED, GEMM16_NN, GEMM16_TN };
+struct Gemm16Plan {
+  Gemm16Op op;
+  bool swap;     // the weight is the MMA's 128-row operand, the tokens its N
+  int bn;        // MMA N: 128 or 256 (pair form), 16, 32, 64 or 128 (swapped)
+  int splits;    // CTAs (pairs) a tile's reduction is split over
+};
+struct Gemm16Params {
+  int M, N;                    // rows and columns of the output
+  int tiles_m, tiles_n;        // tiles along the MMA's M and N
+  int tiles_m1;                // row blocks of the first of two stacked A operands (tiles_m: one)
+  int nk1, nk;                 // 64-wide k-tiles of the first operand pair, of both
+  int splits;                  // set by the launcher
+  int fp16;                    // 0 bf16, 1 fp16
+  int act;                     // svdq_epilogue
+  const uint16_t *bias, *bias2;
+  const uint16_t* R;           // residual rows of stride ldr, or null
+  long long ldr;
+  uint16_t *Y, *Y2;            // output rows of stride ldy; the second stacked output
+  long long ldy;
+  uint16_t *Z, *Z2;            // pre-activations [M][N], or null
+  DeviceErr err;
+};
+// Tensor maps: A, second A, B, second B.
+cudaError_t launch_gemm16(const Gemm16Plan& plan, const CUtensorMap (&tm)[4], Gemm16Params p, int num_sms,
+                          cudaStream_t stream);
+
+// ---------------------------------------------------------------- column sums and activation slopes (act_grad.cu)
+// Kinds of the pass over [M][N] gradients: column sums alone; dZ = dY act'(Z);
+// dG = dH U act'(G), dU = dH act(G); the last two with optional column sums.
+enum ActGradKind { ACT_GRAD_SUM, ACT_GRAD_DENSE, ACT_GRAD_GATED };
+struct ActGradParams {
+  ActGradKind kind;
+  int M, N, fp16, act;
+  const uint16_t* dY;          // rows of stride ld
+  long long ld;
+  const uint16_t *Z, *U;       // [M][N]
+  uint16_t *dZ, *dU;           // [M][N]
+  float *part, *part2;         // [parts][N] column-sum partials, or null
+  int parts;                   // act_grad_parts(M, N)
+};
+int act_grad_parts(int M, int N);
+cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream);
+// out[n] = round(sum over parts, in order, of part[.][n]), dt svdq_dtype
+cudaError_t launch_sum_parts(const float* part, int parts, int N, int dt, void* out, const float* part2, void* out2,
+                             cudaStream_t stream);
+
+// ---------------------------------------------------------------- layer norm (layernorm.cu)
+struct LayerNormParams {
+  int M, C, dt;                // svdq_dtype
+  const void *X, *gamma, *beta;
+  long long ldx, ldy;
+  float eps;
+  void* Y;
+  float *mean, *rstd;          // [M], or null
+};
+cudaError_t launch_layernorm(const LayerNormParams& p, cudaStream_t stream);
+struct LayerNormGradParams {
+  int M, C, dt;
+  const void *dY, *X, *gamma;
+  long long lddy, ldx, lddx;
+  const float *mean, *rstd;
+  void* dX;
+  float *part_g, *part_b;      // [parts][C] partials of dgamma / dbeta, or null
+  int parts;                   // layernorm_grad_parts(M, C)
+};
+int layernorm_grad_parts(int M, int C);
+cudaError_t launch_layernorm_grad(const LayerNormGradParams& p, cudaStream_t stream);
 
 }  // namespace svdq
