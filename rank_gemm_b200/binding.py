@@ -132,7 +132,7 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(s) -> Optional[int]:
     if s is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
 
 

@@ -110,29 +110,35 @@ __global__ void __launch_bounds__(THREADS) act_grad_kernel(ActGradParams p) {
   if (KIND == ACT_GRAD_GATED) reduce(s2, p.part2);
 }
 
-// 32 columns x 8 part lanes a block: lane l adds parts l, l + 8, ..., then the
-// eight in order.
-__global__ void __launch_bounds__(THREADS) sum_parts_kernel(const float* part, const float* part2, int parts, int N,
-                                                            int dt, void* out, void* out2) {
+// 32 columns x 32 part lanes a block: lane l adds parts l, l + 32, ..., then
+// the lanes in order.
+constexpr int SUM_LANES = 32;
+__global__ void __launch_bounds__(32 * SUM_LANES) sum_parts_kernel(const float* part, const float* part2, int parts,
+                                                                   int N, int dt, void* out, void* out2) {
+  grid_dependency_wait();   // launched early: the partials' kernel may still run
   const float* src = blockIdx.y ? part2 : part;
   void* dst = blockIdx.y ? out2 : out;
   const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5, n = blockIdx.x * 32 + cl;
   float t = 0.f;
-  if (n < N)
-    for (int s = rl; s < parts; s += 8) t += src[(size_t)s * N + n];
-  __shared__ float sh[8][32];
+  if (n < N) {
+#pragma unroll 4
+    for (int s = rl; s < parts; s += SUM_LANES) t += src[(size_t)s * N + n];
+  }
+  __shared__ float sh[SUM_LANES][33];
   sh[rl][cl] = t;
   __syncthreads();
-  if (rl == 0 && n < N) {
-    t = 0.f;
+  // warp w takes column w: its 32 lanes' sums, added as a tree
+  t = sh[cl][rl];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) t += sh[r][cl];
+  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  const int col = blockIdx.x * 32 + rl;
+  if (cl == 0 && col < N) {
     if (dt == SVDQ_FP32)
-      static_cast<float*>(dst)[n] = t;
+      static_cast<float*>(dst)[col] = t;
     else if (dt == SVDQ_FP16)
-      static_cast<__half*>(dst)[n] = __float2half_rn(t);
+      static_cast<__half*>(dst)[col] = __float2half_rn(t);
     else
-      static_cast<__nv_bfloat16*>(dst)[n] = __float2bfloat16_rn(t);
+      static_cast<__nv_bfloat16*>(dst)[col] = __float2bfloat16_rn(t);
   }
 }
 
@@ -160,8 +166,16 @@ cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream) {
 
 cudaError_t launch_sum_parts(const float* part, int parts, int N, int dt, void* out, const float* part2, void* out2,
                              cudaStream_t stream) {
-  sum_parts_kernel<<<dim3((N + 31) / 32, part2 ? 2 : 1), THREADS, 0, stream>>>(part, part2, parts, N, dt, out, out2);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((N + 31) / 32, part2 ? 2 : 1);
+  cfg.blockDim = dim3(32 * SUM_LANES);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sum_parts_kernel, part, part2, parts, N, dt, out, out2);
 }
 
 }  // namespace svdq

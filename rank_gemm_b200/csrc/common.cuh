@@ -46,6 +46,20 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return u;
 }
 
+// Read-only loads of data no kernel writes meanwhile.  Volatile, so that a
+// load guarded by a null check is never issued ahead of the check; without a
+// memory clobber, so that it may still move ahead of earlier stores.
+__device__ __forceinline__ uint4 ld_nc(const uint4* p) {
+  uint4 u;
+  asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  return u;
+}
+__device__ __forceinline__ uint16_t ld_nc(const uint16_t* p) {
+  uint16_t u;
+  asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(u) : "l"(p));
+  return u;
+}
+
 // ----------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");

@@ -81,8 +81,14 @@ svdq_status run_gemm(const DeviceInfo& d, const Gemm16Plan& plan, svdq_dtype dt,
   auto map = [&](CUtensorMap* m, const Operand& o, uint32_t box) {
     return encode_tensor_map_2d(m, t, o.ptr, o.inner, o.rows, o.ld * 2, 64, box);
   };
-  if (!map(&tm[0], a0, a_box) || !map(&tm[1], a1 ? *a1 : a0, a_box) || !map(&tm[2], b0, b_box) ||
-      !map(&tm[3], b1 ? *b1 : b0, b_box))
+  if (!map(&tm[0], a0, a_box) || !map(&tm[2], b0, b_box)) return SVDQ_ERR_CUDA;
+  if (!a1)
+    tm[1] = tm[0];
+  else if (!map(&tm[1], *a1, a_box))
+    return SVDQ_ERR_CUDA;
+  if (!b1)
+    tm[3] = tm[2];
+  else if (!map(&tm[3], *b1, b_box))
     return SVDQ_ERR_CUDA;
   p.fp16 = dt == SVDQ_FP16;
   p.err = d.err;
@@ -382,12 +388,12 @@ svdq_status svdq_layernorm_backward(svdq_dtype dt, int M, int C, const void* dY,
     return s != SVDQ_OK ? s : cuda_status(zero(dbeta, (size_t)C * elem_bytes(dt), stream));
   }
   if (!dX && !dgamma) return SVDQ_OK;
-  const int parts = layernorm_grad_parts(M, C);
+  int parts = layernorm_grad_parts(M, C);
   float* pg = dgamma ? static_cast<float*>(workspace) : nullptr;
   float* pb = dgamma ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256((size_t)parts * C * 4))
                      : nullptr;
   s = cuda_status(launch_layernorm_grad(
-      {M, C, (int)dt, dY, X, gamma, lddy, ldx, lddx, mean, rstd, dX, pg, pb, parts}, stream));
+      {M, C, (int)dt, dY, X, gamma, lddy, ldx, lddx, mean, rstd, dX, pg, pb}, &parts, stream));
   if (s != SVDQ_OK || !dgamma) return s;
   return cuda_status(launch_sum_parts(pg, parts, C, dt, dgamma, pb, dbeta, stream));
 }

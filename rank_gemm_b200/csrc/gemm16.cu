@@ -31,6 +31,8 @@
 // partial tiles are summed in rank order through distributed shared memory
 // (no workspace, no atomics, the same bits on every run).
 // All waits are bounded (mbar_wait); TMEM is freed on every exit path.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -165,14 +167,14 @@ __device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 __device__ __forceinline__ float load16(const uint16_t* p, bool fp16) {
-  return unpack16((uint32_t)__ldg(p), fp16).x;
+  return unpack16((uint32_t)ld_nc(p), fp16).x;
 }
 __device__ __forceinline__ uint16_t round16(float v, bool fp16) { return (uint16_t)pack16(v, 0.f, fp16); }
 
 // Eight consecutive columns of one row: v += bias.
 __device__ __forceinline__ void add_bias8(float (&v)[8], const uint16_t* bias, int n, bool fp16) {
   if (!bias) return;
-  const uint4 b = __ldg(reinterpret_cast<const uint4*>(bias + n));
+  const uint4 b = ld_nc(reinterpret_cast<const uint4*>(bias + n));
   const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -349,50 +351,66 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
   const int row = sub * 32 + lane;                            // TMEM lane: row of this CTA's 128
   const bool fp16 = p.fp16 != 0;
 
-  // rows x 8 columns of an output tile (pair form): row m, columns n .. n + 7
-  auto emit8 = [&](uint16_t* out, int m, int n, float (&v)[8], float (&u)[8]) {
+  // Eight columns n .. n + 7 of row m (pair form), r the residual's.
+  auto emit8 = [&](uint16_t* out, int m, int n, float (&v)[8], float (&u)[8], const uint4& r) {
+    add_bias8(v, p.bias, n, fp16);
+    if (GATED) add_bias8(u, p.bias2, n, fp16);
+    const size_t at = (size_t)m * p.N + n;
+    if (p.Z) store8(p.Z + at, v, fp16);
+    if (GATED && p.Z2) store8(p.Z2 + at, u, fp16);
+    act8(v, p.act);
     if (GATED) {
-      add_bias8(v, p.bias, n, fp16);
-      add_bias8(u, p.bias2, n, fp16);
-      const size_t at = (size_t)m * p.N + n;
-      if (p.Z) store8(p.Z + at, v, fp16);
-      if (p.Z2) store8(p.Z2 + at, u, fp16);
-      act8(v, p.act);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= u[i];
-    } else {
-      add_bias8(v, p.bias, n, fp16);
-      if (p.Z) store8(p.Z + (size_t)m * p.N + n, v, fp16);
-      act8(v, p.act);
-      if (p.R) {
-        const uint4 r = *reinterpret_cast<const uint4*>(p.R + (size_t)m * p.ldr + n);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    } else if (p.R) {
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = unpack16(w[i], fp16);
-          v[2 * i] += f.x;
-          v[2 * i + 1] += f.y;
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack16(w[i], fp16);
+        v[2 * i] += f.x;
+        v[2 * i + 1] += f.y;
       }
     }
     store8(out + (size_t)m * p.ldy + n, v, fp16);
   };
-  // one value (swapped form): token m, feature n; the warp's 32 lanes are 32 consecutive features
-  auto emit1 = [&](int m, int n, float v, float u) {
-    if (p.bias) v += load16(p.bias + n, fp16);
-    if (GATED) {
-      if (p.bias2) u += load16(p.bias2 + n, fp16);
-      const size_t at = (size_t)m * p.N + n;
-      if (p.Z) p.Z[at] = round16(v, fp16);
-      if (p.Z2) p.Z2[at] = round16(u, fp16);
-    } else if (p.Z) {
-      p.Z[(size_t)m * p.N + n] = round16(v, fp16);
+  // The residual of eight columns; the pointers may be Y's own, so it is
+  // loaded before anything of its chunk is stored.
+  auto residual8 = [&](int m, int n) {
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (!GATED && p.R && m < p.M && n < p.N) r = *reinterpret_cast<const uint4*>(p.R + (size_t)m * p.ldr + n);
+    return r;
+  };
+  // COUNT tokens m0, m0 + step, ... of feature n (swapped form): a warp's
+  // lanes are 32 consecutive features.
+  float bias_v = 0.f, bias_u = 0.f;
+  auto load_bias = [&](int n) {
+    if (n < p.N) {
+      if (p.bias) bias_v = load16(p.bias + n, fp16);
+      if (GATED && p.bias2) bias_u = load16(p.bias2 + n, fp16);
     }
-    if (p.act == SVDQ_EPI_GELU_TANH) v = gelu_tanh(v);
-    if (p.act == SVDQ_EPI_SILU) v = silu(v);
-    if (GATED) v *= u;
-    if (!GATED && p.R) v += unpack16((uint32_t)p.R[(size_t)m * p.ldr + n], fp16).x;
-    p.Y[(size_t)m * p.ldy + n] = round16(v, fp16);
+  };
+  auto emit_tokens = [&](int m0, int step, int n, const float* v, const float* u, auto count) {
+    constexpr int COUNT = decltype(count)::value;
+    float r[COUNT];
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      const int m = m0 + i * step;
+      r[i] = (!GATED && p.R && m < p.M && n < p.N) ? unpack16((uint32_t)p.R[(size_t)m * p.ldr + n], fp16).x : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      const int m = m0 + i * step;
+      if (m >= p.M || n >= p.N) continue;
+      float f = v[i] + bias_v;
+      const float g = GATED ? u[i] + bias_u : 0.f;
+      const size_t at = (size_t)m * p.N + n;
+      if (p.Z) p.Z[at] = round16(f, fp16);
+      if (GATED && p.Z2) p.Z2[at] = round16(g, fp16);
+      if (p.act == SVDQ_EPI_GELU_TANH) f = gelu_tanh(f);
+      if (p.act == SVDQ_EPI_SILU) f = silu(f);
+      f = GATED ? f * g : f + r[i];
+      p.Y[(size_t)m * p.ldy + n] = round16(f, fp16);
+    }
   };
 
   if (warp >= 2 && S == 1) {
@@ -403,22 +421,34 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
       const bool second = mb >= p.tiles_m1;
       const int row0 = (second ? mb - p.tiles_m1 : mb) * 128 * CG + cta * 128;
       const uint32_t ab = tl & 1, pt = (tl >> 1) & 1;
+      constexpr int PER = OUT_COLS / 2;                       // pair form: columns of this warp
+      const int c0 = (e >> 2) * PER, m = row0 + row, n_tile = nb * OUT_COLS;
+      uint4 res[2];
+      if (!SWAP) {
+        res[0] = residual8(m, n_tile + c0);
+        res[1] = residual8(m, n_tile + c0 + 8);
+      } else {
+        load_bias(m);
+      }
       if (!mbar_wait(smem_u32(&ctl->t_full[ab]), pt, abort_flag, p.err)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16) + ab * C::ACC_COLS;
       if (!SWAP) {
-        constexpr int PER = OUT_COLS / 2;                     // columns of this warp
-        const int c0 = (e >> 2) * PER, m = row0 + row;
         uint16_t* out = second ? p.Y2 : p.Y;
 #pragma unroll 1
         for (int c = c0; c < c0 + PER; c += 16) {
           uint32_t r[16], q[16];
           tmem_ld16(taddr + c, r);
           if (GATED) tmem_ld16(taddr + BN / 2 + c, q);
+          const uint4 now[2] = {res[0], res[1]};
+          if (c + 16 < c0 + PER) {
+            res[0] = residual8(m, n_tile + c + 16);
+            res[1] = residual8(m, n_tile + c + 24);
+          }
           tmem_wait_ld();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int n = nb * OUT_COLS + c + 8 * h;
+            const int n = n_tile + c + 8 * h;
             if (m < p.M && n < p.N) {
               float v[8], u[8];
 #pragma unroll
@@ -426,24 +456,19 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
                 v[i] = __uint_as_float(r[8 * h + i]);
                 u[i] = GATED ? __uint_as_float(q[8 * h + i]) : 0.f;
               }
-              emit8(out, m, n, v, u);
+              emit8(out, m, n, v, u, now[h]);
             }
           }
         }
       } else {
-        const int n = row0 + row;                             // feature
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 16) {
-          const int m0 = nb * BN + c;                         // token
-          if (m0 >= p.M) break;
+        for (int c = 0; c < BN && nb * BN + c < p.M; c += 16) {
           uint32_t r[16], q[16];
           tmem_ld16(taddr + c, r);
           if (GATED) tmem_ld16(taddr + BN + c, q);
           tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (m0 + i < p.M && n < p.N)
-              emit1(m0 + i, n, __uint_as_float(r[i]), GATED ? __uint_as_float(q[i]) : 0.f);
+          emit_tokens(nb * BN + c, 1, m, reinterpret_cast<const float*>(r), reinterpret_cast<const float*>(q),
+                      std::integral_constant<int, 16>{});
         }
       }
       tc_fence_before();
@@ -459,16 +484,22 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
   if (S > 1) {
     // One tile per cluster: every CTA parks its float32 partial in its own
     // ring (free: all of its MMAs are complete) as [column][128 rows], and
-    // rank s sums columns s, s + S, ... (in blocks of 8 in the pair form) of
-    // all ranks in rank order.
+    // rank s sums columns s, s + S, ... (blocks of 8 in the pair form) of all
+    // ranks in rank order, eight loads in flight a thread.
     const uint32_t part = smem_u32(ring);
+    int mb, nb;
+    coords(first, mb, nb);
+    const bool second = mb >= p.tiles_m1;
+    const int m = (second ? mb - p.tiles_m1 : mb) * 128 * CG + cta * 128 + row;
     bool ok = false;
     if (warp >= 2) {
+      if (SWAP) load_bias(m);
       ok = mbar_wait(smem_u32(&ctl->t_full[0]), 0, abort_flag, p.err);
       if (ok) {
         tc_fence_after();
         const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16);
         for (int c = (e >> 2) * 16; c < C::ACC_COLS; c += 16 * (C::EPI_WARPS / 4)) {
+          if (SWAP && nb * BN + (c & (BN - 1)) >= p.M) continue;   // columns past the last token
           uint32_t r[16];
           tmem_ld16(taddr + c, r);
           tmem_wait_ld();
@@ -480,34 +511,44 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
     }
     cluster_sync_all();
     if (warp >= 2 && ok) {
-      int mb, nb;
-      coords(first, mb, nb);
-      const bool second = mb >= p.tiles_m1;
-      const int row0 = (second ? mb - p.tiles_m1 : mb) * 128 * CG + cta * 128;
-      auto total = [&](int col) {
-        float v = 0.f;
-        for (int s = 0; s < S; ++s) v += ld_dsmem_f32(dsmem_map(part + (col * 128 + row) * 4, s * CG + cta));
-        return v;
+      // columns col, col + step, ... (8, none past `last`) summed over the ranks
+      auto totals = [&](int col, int step, int last, float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        for (int s = 0; s < S; ++s) {
+          const uint32_t from = dsmem_map(part + row * 4, s * CG + cta);
+          float t[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[i] = ld_dsmem_f32(from + min(col + i * step, last) * 512);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += t[i];
+        }
       };
       if (!SWAP) {
-        const int m = row0 + row;
         uint16_t* out = second ? p.Y2 : p.Y;
         for (int b = (e >> 2) * S + split; b < OUT_COLS / 8; b += 2 * S) {
           const int n = nb * OUT_COLS + 8 * b;
           if (m < p.M && n < p.N) {
+            const uint4 res = residual8(m, n);
             float v[8], u[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              v[i] = total(8 * b + i);
-              u[i] = GATED ? total(BN / 2 + 8 * b + i) : 0.f;
-            }
-            emit8(out, m, n, v, u);
+            totals(8 * b, 1, C::ACC_COLS - 1, v);
+            if (GATED) totals(BN / 2 + 8 * b, 1, C::ACC_COLS - 1, u);
+            emit8(out, m, n, v, u, res);
           }
         }
       } else {
-        const int n = row0 + row;
-        for (int c = split; c < BN && nb * BN + c < p.M; c += S)
-          if (n < p.N) emit1(nb * BN + c, n, total(c), GATED ? total(BN + c) : 0.f);
+        for (int c = split; c < BN && nb * BN + c < p.M; c += 8 * S) {
+          float v[8], u[8];
+          totals(c, S, BN - 1, v);
+          if (GATED) totals(BN + c, S, 2 * BN - 1, u);
+          // fewer than 8 of this rank's columns are left in the tile: one by one
+          const int left = (BN - c + S - 1) / S;
+          if (left >= 8)
+            emit_tokens(nb * BN + c, S, m, v, u, std::integral_constant<int, 8>{});
+          else
+            for (int i = 0; i < 8; ++i)
+              if (i < left) emit_tokens(nb * BN + c + i * S, 1, m, v + i, u + i, std::integral_constant<int, 1>{});
+        }
       }
     }
   }

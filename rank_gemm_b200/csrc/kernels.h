@@ -306,9 +306,9 @@ struct LayerNormGradParams {
   const float *mean, *rstd;
   void* dX;
   float *part_g, *part_b;      // [parts][C] partials of dgamma / dbeta, or null
-  int parts;                   // layernorm_grad_parts(M, C)
 };
-int layernorm_grad_parts(int M, int C);
-cudaError_t launch_layernorm_grad(const LayerNormGradParams& p, cudaStream_t stream);
+int layernorm_grad_parts(int M, int C);   // partials at most
+// *parts: the partials it writes
+cudaError_t launch_layernorm_grad(const LayerNormGradParams& p, int* parts, cudaStream_t stream);
 
 }  // namespace svdq
