@@ -221,8 +221,9 @@ svdq_status svdq::current_device_info(DeviceInfo* info) {
 }
 
 bool svdq::encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inner,
-                                uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows) {
-  return tmap_2d(m, dt, ptr, inner, rows, row_bytes, box_inner, box_rows);
+                                uint64_t rows, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows,
+                                CUtensorMapSwizzle swizzle) {
+  return tmap_2d(m, dt, ptr, inner, rows, row_bytes, box_inner, box_rows, swizzle);
 }
 
 svdq_status svdq::cuda_status(cudaError_t e) { return from_cuda(e); }

@@ -77,7 +77,7 @@ svdq_status run_gemm(const DeviceInfo& d, const Gemm16Plan& plan, svdq_dtype dt,
   const bool a_mn = plan.op == GEMM16_TN || (plan.swap && plan.op == GEMM16_NN);
   const bool b_mn = plan.op == GEMM16_TN || (!plan.swap && plan.op == GEMM16_NN);
   const uint32_t a_box = a_mn ? 64 : 128, b_box = b_mn ? 64 : plan.swap ? plan.bn : plan.bn / 2;
-  CUtensorMap tm[4];
+  CUtensorMap tm[7];
   auto map = [&](CUtensorMap* m, const Operand& o, uint32_t box) {
     return encode_tensor_map_2d(m, t, o.ptr, o.inner, o.rows, o.ld * 2, 64, box);
   };
@@ -90,6 +90,20 @@ svdq_status run_gemm(const DeviceInfo& d, const Gemm16Plan& plan, svdq_dtype dt,
     tm[3] = tm[2];
   else if (!map(&tm[3], *b1, b_box))
     return SVDQ_ERR_CUDA;
+  if (!plan.swap) {   // the outputs' store boxes; maps that nothing uses are copies
+    const uint32_t w = gemm16_box_cols(plan);
+    auto out = [&](CUtensorMap* m, void* ptr, uint64_t ld) {
+      return encode_tensor_map_2d(m, t, ptr, p.N, p.M, ld * 2, w, 32,
+                                  w == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+    };
+    void* z2 = p.Z2 ? p.Z2 : p.Y2;
+    if (!out(&tm[4], p.Y, p.ldy)) return SVDQ_ERR_CUDA;
+    tm[5] = tm[6] = tm[4];
+    if (p.Z && !out(&tm[5], p.Z, p.N)) return SVDQ_ERR_CUDA;
+    if (z2 && !out(&tm[6], z2, p.Z2 ? (uint64_t)p.N : (uint64_t)p.ldy)) return SVDQ_ERR_CUDA;
+  } else {
+    tm[4] = tm[5] = tm[6] = tm[0];
+  }
   p.fp16 = dt == SVDQ_FP16;
   p.err = d.err;
   return cuda_status(launch_gemm16(plan, tm, p, d.num_sms, stream));

@@ -30,6 +30,8 @@
 // Few tiles: the reduction is split over the CTAs of a cluster, whose float32
 // partial tiles are summed in rank order through distributed shared memory
 // (no workspace, no atomics, the same bits on every run).
+// Outputs of whole tiles leave through shared memory, a 32-row box of 128-byte
+// rows per warp and TMA store, so they reach L2 as full lines.
 // All waits are bounded (mbar_wait); TMEM is freed on every exit path.
 #include <type_traits>
 
@@ -60,13 +62,16 @@ struct Cfg {
   static constexpr int B_ROWS = BN / CG;                  // per CTA
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int ROOM = (SMEM_LIMIT - 1024 - (int)sizeof(Ctl)) / STAGE;
+  static constexpr int OUT_COLS = (GATED && !SWAP) ? BN / 2 : BN;   // output columns of a tile
+  static constexpr int BOX_COLS = OUT_COLS / 2 < 64 ? OUT_COLS / 2 : 64;   // pair form: columns of a store box
+  static constexpr int EPI_WARPS = SWAP ? 4 : 8;          // one or two per TMEM sub-partition
+  static constexpr int PARK = SWAP ? 0 : EPI_WARPS * 32 * BOX_COLS * 2;   // one store box a warp
+  static constexpr int ROOM = (SMEM_LIMIT - 1024 - PARK - (int)sizeof(Ctl)) / STAGE;
   static constexpr int STAGES = ROOM < MAX_STAGES ? ROOM : MAX_STAGES;
   static constexpr int ACC_COLS = A_TILES * BN;
   static constexpr int TMEM_COLS = pow2_at_least(2 * ACC_COLS, 32);
-  static constexpr int EPI_WARPS = SWAP ? 4 : 8;          // one or two per TMEM sub-partition
   static constexpr int THREADS = 32 * (2 + EPI_WARPS);
-  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + sizeof(Ctl);
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + PARK + sizeof(Ctl);
   static_assert(STAGE % 1024 == 0, "tiles stay 1024-byte aligned for the 128-byte swizzle");
   static_assert(TMEM_COLS <= 512 && STAGES >= 3, "TMEM or ring too small");
   static_assert(ACC_COLS * 512 <= STAGES * STAGE, "a split's partial tile fits the ring");
@@ -85,6 +90,19 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(cluster_bar)
       : "memory");
+}
+// Store of a box from shared memory; rows and columns past the tensor are left out.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
@@ -183,9 +201,21 @@ __device__ __forceinline__ void add_bias8(float (&v)[8], const uint16_t* bias, i
     v[2 * i + 1] += f.y;
   }
 }
+__device__ __forceinline__ uint4 round8(const float (&v)[8], bool fp16) {
+  return make_uint4(pack16(v[0], v[1], fp16), pack16(v[2], v[3], fp16), pack16(v[4], v[5], fp16),
+                    pack16(v[6], v[7], fp16));
+}
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8], bool fp16) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack16(v[0], v[1], fp16), pack16(v[2], v[3], fp16),
-                                            pack16(v[4], v[5], fp16), pack16(v[6], v[7], fp16));
+  *reinterpret_cast<uint4*>(p) = round8(v, fp16);
+}
+__device__ __forceinline__ void add8(float (&v)[8], const uint4& r, bool fp16) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack16(w[i], fp16);
+    v[2 * i] += f.x;
+    v[2 * i + 1] += f.y;
+  }
 }
 __device__ __forceinline__ void act8(float (&v)[8], int act) {
   if (act == SVDQ_EPI_GELU_TANH) {
@@ -202,12 +232,15 @@ __device__ __forceinline__ void act8(float (&v)[8], int act) {
 template <int CG, int BN, bool SWAP, bool GATED, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
     gemm16_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
-                  const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, Gemm16Params p) {
+                  const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+                  const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
+                  const __grid_constant__ CUtensorMap tmZ2, Gemm16Params p) {
   using C = Cfg<CG, BN, SWAP, GATED>;
-  constexpr int OUT_COLS = (GATED && !SWAP) ? BN / 2 : BN;   // output columns of a tile
+  constexpr int OUT_COLS = C::OUT_COLS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Ctl* ctl = reinterpret_cast<Ctl*>(ring + C::STAGES * C::STAGE);
+  uint8_t* park = ring + C::STAGES * C::STAGE;
+  Ctl* ctl = reinterpret_cast<Ctl*>(park + C::PARK);
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -236,6 +269,10 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
+  // The next kernel may be scheduled as SMs fall idle; this one touches
+  // global memory only after the previous kernel's writes are visible.
+  grid_launch_dependents();
+  if (warp != 1) grid_dependency_wait();
 
   const int num_tiles = p.tiles_m * p.tiles_n;
   const int first = (int)blockIdx.x / (CG * S), step = (int)gridDim.x / (CG * S);
@@ -363,13 +400,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= u[i];
     } else if (p.R) {
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack16(w[i], fp16);
-        v[2 * i] += f.x;
-        v[2 * i + 1] += f.y;
-      }
+      add8(v, r, fp16);
     }
     store8(out + (size_t)m * p.ldy + n, v, fp16);
   };
@@ -421,44 +452,77 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
       const bool second = mb >= p.tiles_m1;
       const int row0 = (second ? mb - p.tiles_m1 : mb) * 128 * CG + cta * 128;
       const uint32_t ab = tl & 1, pt = (tl >> 1) & 1;
-      constexpr int PER = OUT_COLS / 2;                       // pair form: columns of this warp
-      const int c0 = (e >> 2) * PER, m = row0 + row, n_tile = nb * OUT_COLS;
+      const int m = row0 + row;                               // pair form: row; swapped: feature
+      if (SWAP) load_bias(m);
+      // pair form: this warp's 32 rows, columns c0 .. c0 + PER - 1 of the tile, in boxes of W
+      constexpr int PER = OUT_COLS / 2, W = C::BOX_COLS;
+      const int c0 = (e >> 2) * PER, n_tile = nb * OUT_COLS, row_w = row0 + sub * 32;
       uint4 res[2];
       if (!SWAP) {
         res[0] = residual8(m, n_tile + c0);
         res[1] = residual8(m, n_tile + c0 + 8);
-      } else {
-        load_bias(m);
       }
       if (!mbar_wait(smem_u32(&ctl->t_full[ab]), pt, abort_flag, p.err)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16) + ab * C::ACC_COLS;
       if (!SWAP) {
-        uint16_t* out = second ? p.Y2 : p.Y;
+        const uint32_t box = smem_u32(park) + (uint32_t)e * (32 * W * 2);
+        // one output of a W-column box: what(v, u, n, res) turns eight columns' accumulators into its values
+        auto emit_box = [&](const CUtensorMap* map, int c, bool last, auto what) {
+          if (lane == 0) bulk_wait_read();   // the previous box has left shared memory
+          __syncwarp();
 #pragma unroll 1
-        for (int c = c0; c < c0 + PER; c += 16) {
-          uint32_t r[16], q[16];
-          tmem_ld16(taddr + c, r);
-          if (GATED) tmem_ld16(taddr + BN / 2 + c, q);
-          const uint4 now[2] = {res[0], res[1]};
-          if (c + 16 < c0 + PER) {
-            res[0] = residual8(m, n_tile + c + 16);
-            res[1] = residual8(m, n_tile + c + 24);
-          }
-          tmem_wait_ld();
+          for (int d = 0; d < W; d += 16) {
+            uint32_t r[16], q[16];
+            tmem_ld16(taddr + c + d, r);
+            if (GATED) tmem_ld16(taddr + BN / 2 + c + d, q);
+            const uint4 now[2] = {res[0], res[1]};
+            if (last && c + d + 16 < c0 + PER) {
+              res[0] = residual8(m, n_tile + c + d + 16);
+              res[1] = residual8(m, n_tile + c + d + 24);
+            }
+            tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int n = n_tile + c + 8 * h;
-            if (m < p.M && n < p.N) {
+            for (int h = 0; h < 2; ++h) {
               float v[8], u[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 v[i] = __uint_as_float(r[8 * h + i]);
                 u[i] = GATED ? __uint_as_float(q[8 * h + i]) : 0.f;
               }
-              emit8(out, m, n, v, u, now[h]);
+              const int n = n_tile + c + d + 8 * h;
+              if (n < p.N) {
+                add_bias8(v, p.bias, n, fp16);
+                if (GATED) add_bias8(u, p.bias2, n, fp16);
+              }
+              what(v, u, now[h]);
+              const int chunk = (d >> 3) + h;   // 16-byte chunk of the row, swizzled as the box's map
+              const uint32_t at = W == 64 ? lane * 128 + ((chunk ^ (lane & 7)) << 4)
+                                          : lane * 64 + ((chunk ^ ((lane >> 1) & 3)) << 4);
+              sts128(box + at, round8(v, fp16));
             }
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row_w < p.M && n_tile + c < p.N) tma_store_2d(map, box, n_tile + c, row_w);
+        };
+#pragma unroll 1
+        for (int c = c0; c < c0 + PER; c += W) {
+          if (p.Z) emit_box(&tmZ, c, false, [&](float (&)[8], float (&)[8], const uint4&) {});
+          if (GATED && p.Z2)
+            emit_box(&tmZ2, c, false, [&](float (&v)[8], float (&u)[8], const uint4&) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = u[i];
+            });
+          emit_box(!GATED && second ? &tmZ2 : &tmY, c, true, [&](float (&v)[8], float (&u)[8], const uint4& r) {
+            act8(v, p.act);
+            if (GATED) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] *= u[i];
+            } else if (p.R) {
+              add8(v, r, fp16);
+            }
+          });
         }
       } else {
 #pragma unroll 1
@@ -480,6 +544,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
           mbar_arrive(smem_u32(&ctl->t_empty[ab]));
       }
     }
+    if (!SWAP && lane == 0) bulk_wait_all();
   }
   if (S > 1) {
     // One tile per cluster: every CTA parks its float32 partial in its own
@@ -568,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
 namespace {
 
 template <int CG, int BN, bool SWAP, bool GATED, bool A_MN, bool B_MN>
-cudaError_t launch(const CUtensorMap (&tm)[4], const Gemm16Params& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap (&tm)[7], const Gemm16Params& p, int num_sms, cudaStream_t stream) {
   using C = Cfg<CG, BN, SWAP, GATED>;
   auto kern = gemm16_kernel<CG, BN, SWAP, GATED, A_MN, B_MN>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM);
@@ -581,19 +646,21 @@ cudaError_t launch(const CUtensorMap (&tm)[4], const Gemm16Params& p, int num_sm
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = width;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], p);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], tm[6], p);
 }
 
 }  // namespace
 
-cudaError_t launch_gemm16(const Gemm16Plan& plan, const CUtensorMap (&tm)[4], Gemm16Params p, int num_sms,
+cudaError_t launch_gemm16(const Gemm16Plan& plan, const CUtensorMap (&tm)[7], Gemm16Params p, int num_sms,
                           cudaStream_t stream) {
   p.splits = plan.splits;
   if (plan.swap) {

@@ -33,7 +33,8 @@ svdq_status current_device_info(DeviceInfo* info);
 // 2-D tensor map over row-major [rows][inner], 128-byte swizzled boxes; false
 // when the driver refuses it.
 bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t rows,
-                          uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows);
+                          uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows,
+                          CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 // A CUDA status as an entry point returns it (clears a non-sticky error).
 svdq_status cuda_status(cudaError_t e);
@@ -265,8 +266,10 @@ struct Gemm16Params {
   uint16_t *Z, *Z2;            // pre-activations [M][N], or null
   DeviceErr err;
 };
-// Tensor maps: A, second A, B, second B.
-cudaError_t launch_gemm16(const Gemm16Plan& plan, const CUtensorMap (&tm)[4], Gemm16Params p, int num_sms,
+// Columns of the pair form's store boxes (32 rows high; 128-byte swizzle, 64-byte for 32 columns).
+constexpr int gemm16_box_cols(const Gemm16Plan& p) { return p.op == GEMM16_GATED && p.bn == 128 ? 32 : 64; }
+// Tensor maps: A, second A, B, second B; Y, Z, and Z2 or the second stacked output.
+cudaError_t launch_gemm16(const Gemm16Plan& plan, const CUtensorMap (&tm)[7], Gemm16Params p, int num_sms,
                           cudaStream_t stream);
 
 // ---------------------------------------------------------------- column sums and activation slopes (act_grad.cu)
