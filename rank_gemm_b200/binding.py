@@ -132,7 +132,7 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(s) -> Optional[int]:
     if s is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
 
 
@@ -365,7 +365,7 @@ def _workspace(t, ws_bytes, dev):
 def _type_of(t, what):
     if t is None or t.dtype not in DTYPES:
         raise ValueError("svdq: %s has to be a bfloat16, float16 or float32 tensor" % what)
-    return t.dtype, DTYPES[t.dtype], torch.cuda.current_device() if t.is_cuda else -2
+    return t.dtype, DTYPES[t.dtype], torch._C._cuda_getDevice() if t.is_cuda else -2
 
 
 def svdq_dense_linear(M, K, N, X, W_t, bias, act, residual, Y, Z=None, stream=None):

@@ -29,156 +29,216 @@ const uint16_t* in16(const void* p) { return static_cast<const uint16_t*>(p); }
 uint16_t* out16(void* p) { return static_cast<uint16_t*>(p); }
 
 // ------------------------------------------------------------------ tiling
-// A tile's k-tile costs its MMA cycles, or the time its operand bytes take
-// into shared memory where that is longer; a tile also costs a fixed part.
-Gemm16Plan plan_pair(Gemm16Op op, int rows, int cols, int nk, int num_sms) {
-  Gemm16Plan best{op, false, 256, 1};
-  double best_t = 0;
-  const int pairs = num_sms / 2;
+// Clusters of `width` CTAs an SM-filling grid can hold at once: the SMs of a
+// GPC that do not make up a whole cluster stay idle (cudaOccupancy reports
+// 148, 74, 33 and 15 for widths 1, 2, 4 and 8 on this part).
+int clusters(int width, int num_sms) {
+  return width == 1 ? num_sms : width == 2 ? num_sms / 2 : width == 4 ? num_sms * 33 / 148 : num_sms * 15 / 148;
+}
+
+// Estimated time of a plan in SM cycles: rounds of tiles times k-tiles times
+// the cycles of one k-tile, and fixed parts: launch, fill and drain, the
+// exchange of a split tile's partials, the swapped form's epilogue.  The
+// constants fit the times of 17 shapes (1 .. 777 rows, 1024 x 1024 to
+// 12288 x 3072) under every tiling, each within a sixth; a k-tile costs what
+// its operand bytes take into shared memory (40 to 57 bytes a cycle), not its
+// MMAs.  Where the two forms cross (us, best tilings): 64 x 1024 -> 1024
+// swapped 6.1, pair 8.1; 128 x 12288 -> 3072 swapped 25.5, pair 30.2;
+// 256 x 1024 -> 1024 swapped 8.6, pair 8.6; 256 x 3072 -> 9216 swapped 20.3,
+// pair 18.5.
+struct Choice {
+  Gemm16Plan plan{};
+  double cycles = 0;
+  void offer(const Gemm16Plan& p, double t) {
+    if (cycles == 0 || t < cycles) {
+      plan = p;
+      cycles = t;
+    }
+  }
+};
+struct JobShape {
+  int rows, cols, nk;   // row blocks of 256, columns, k-tiles
+};
+Choice plan_pair(Gemm16Op op, JobShape a, JobShape b, int num_sms) {
+  Choice best;
   for (int bn = 256; bn >= 128; bn -= 128) {
     const int out_cols = op == GEMM16_GATED ? bn / 2 : bn;
-    const long long tiles = (long long)rows * ceil_div(cols, out_cols);
+    const double per_k = bn == 256 ? 620 : 480, exchange = bn == 256 ? 12000 : 5000;
+    const long long ta = (long long)a.rows * ceil_div(a.cols, out_cols),
+                    tb = (long long)b.rows * ceil_div(b.cols, out_cols), tiles = ta + tb;
     for (int s = 1; s <= 4; s *= 2) {
-      if (s > 1 && (nk < 4 * s || tiles * s > pairs)) break;
-      const double per_k = bn == 256 ? 512 : 320;
-      const double waves = (double)((tiles * s + pairs - 1) / pairs);
-      const double t = waves * ceil_div(nk, s) * per_k + (s > 1 ? 2500 : 1500);
-      if (best_t == 0 || t < best_t) {
-        best_t = t;
-        best = Gemm16Plan{op, false, bn, s};
-      }
+      const int slots = clusters(2 * s, num_sms);
+      if (s > 1 && ((ta && a.nk < 4 * s) || (tb && b.nk < 4 * s) || tiles > slots)) break;
+      const int ka = ceil_div(a.nk, s), kb = ceil_div(b.nk, s), longest = ka > kb ? ka : kb;
+      // one job's tiles run in whole rounds; two jobs' even out, down to the longest tile
+      double k = tb ? ((double)ta * ka + (double)tb * kb) / slots : (double)((tiles + slots - 1) / slots) * ka;
+      if (k < longest) k = longest;
+      best.offer({op, false, bn, s}, 9500 + k * per_k + (s > 1 ? exchange : 0));
     }
   }
   return best;
 }
-
-Gemm16Plan plan_swap(Gemm16Op op, int tokens, int features, int nk, int num_sms) {
-  int bn = 16;
-  while (bn < 128 && bn < tokens) bn *= 2;
-  const int tiles = ceil_div(features, 128) * ceil_div(tokens, bn);
-  int s = 1;
-  while (s < 8 && tiles * s * 2 <= num_sms && nk >= 4 * s) s *= 2;
-  return Gemm16Plan{op, true, bn, s};
+Choice plan_swap(Gemm16Op op, int tokens, int features, int nk, int num_sms) {
+  Choice best;
+  const int weights = op == GEMM16_GATED ? 2 : 1;
+  const double stream = (double)weights * features * nk * 128 / 3400;   // the weights at HBM's rate
+  for (int bn = 16; bn <= 128; bn *= 2) {
+    const int tiles = ceil_div(features, 128) * ceil_div(tokens, bn);
+    const double per_k = 400 * weights + 1.3 * bn;
+    for (int s = 1; s <= 8 && 4 * s <= bn; s *= 2) {   // at least four tokens a rank
+      const int slots = clusters(s, num_sms);
+      if (s > 1 && (nk < 2 * s || tiles > slots)) break;
+      double t = (double)((tiles + slots - 1) / slots) * ceil_div(nk, s) * per_k;
+      if (t < stream) t = stream;
+      best.offer({op, true, bn, s}, 8500 + t + 15 * bn + (s > 1 ? 1500 + 45 * bn : 0));
+    }
+    if (bn >= tokens) break;
+  }
+  return best;
 }
-// Up to this many rows of X the swapped form is taken.
-constexpr int SWAP_ROWS = 128;
+// More rows of X than this never gain from the swapped form.
+constexpr int SWAP_ROWS = 256;
 
 // ------------------------------------------------------------------ operands
 struct Operand {
   const void* ptr;
   uint64_t inner, rows, ld;   // innermost extent, rows, row stride in elements
 };
+CUtensorMapDataType map_type(svdq_dtype dt) {
+  return dt == SVDQ_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
 
-// Encodes A (128-row tiles) and B (b_rows of them per CTA) and launches.
-svdq_status run_gemm(const DeviceInfo& d, const Gemm16Plan& plan, svdq_dtype dt, const Operand& a0, const Operand* a1,
-                     const Operand& b0, const Operand* b1, Gemm16Params p, cudaStream_t stream) {
-  const CUtensorMapDataType t =
-      dt == SVDQ_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const bool a_mn = plan.op == GEMM16_TN || (plan.swap && plan.op == GEMM16_NN);
-  const bool b_mn = plan.op == GEMM16_TN || (!plan.swap && plan.op == GEMM16_NN);
-  const uint32_t a_box = a_mn ? 64 : 128, b_box = b_mn ? 64 : plan.swap ? plan.bn : plan.bn / 2;
-  CUtensorMap tm[7];
-  auto map = [&](CUtensorMap* m, const Operand& o, uint32_t box) {
-    return encode_tensor_map_2d(m, t, o.ptr, o.inner, o.rows, o.ld * 2, 64, box);
+// A job's maps: operands in boxes of 64 along their inner extent, outputs in
+// the epilogue's store boxes.
+bool encode_job(const Gemm16Plan& plan, svdq_dtype dt, const Operand& a, const Operand* a2, const Operand& b,
+                const Operand* b2, const Gemm16Job& j, void* Z, void* Z2, CUtensorMap* m) {
+  const CUtensorMapDataType t = map_type(dt);
+  const bool grad = plan.op == GEMM16_GRAD;
+  const uint32_t a_box = grad && j.a_mn ? 64 : 128, b_box = grad ? 64 : plan.swap ? plan.bn : plan.bn / 2;
+  auto in = [&](CUtensorMap* to, const Operand& o, uint32_t box) {
+    return encode_tensor_map_2d(to, t, o.ptr, o.inner, o.rows, o.ld * 2, 64, box);
   };
-  if (!map(&tm[0], a0, a_box) || !map(&tm[2], b0, b_box)) return SVDQ_ERR_CUDA;
-  if (!a1)
-    tm[1] = tm[0];
-  else if (!map(&tm[1], *a1, a_box))
-    return SVDQ_ERR_CUDA;
-  if (!b1)
-    tm[3] = tm[2];
-  else if (!map(&tm[3], *b1, b_box))
-    return SVDQ_ERR_CUDA;
-  if (!plan.swap) {   // the outputs' store boxes; maps that nothing uses are copies
-    const uint32_t w = gemm16_box_cols(plan);
-    auto out = [&](CUtensorMap* m, void* ptr, uint64_t ld) {
-      return encode_tensor_map_2d(m, t, ptr, p.N, p.M, ld * 2, w, 32,
-                                  w == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
-    };
-    void* z2 = p.Z2 ? p.Z2 : p.Y2;
-    if (!out(&tm[4], p.Y, p.ldy)) return SVDQ_ERR_CUDA;
-    tm[5] = tm[6] = tm[4];
-    if (p.Z && !out(&tm[5], p.Z, p.N)) return SVDQ_ERR_CUDA;
-    if (z2 && !out(&tm[6], z2, p.Z2 ? (uint64_t)p.N : (uint64_t)p.ldy)) return SVDQ_ERR_CUDA;
-  } else {
-    tm[4] = tm[5] = tm[6] = tm[0];
-  }
-  p.fp16 = dt == SVDQ_FP16;
-  p.err = d.err;
-  return cuda_status(launch_gemm16(plan, tm, p, d.num_sms, stream));
+  const uint32_t cols = plan.swap ? 128 : gemm16_box_cols(plan), rows = plan.swap ? plan.bn / plan.splits : 32;
+  const CUtensorMapSwizzle swz = plan.swap    ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                 : cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                              : CU_TENSOR_MAP_SWIZZLE_64B;
+  auto out = [&](CUtensorMap* to, void* ptr, uint64_t ld) {
+    return encode_tensor_map_2d(to, t, ptr, j.N, j.M, ld * 2, cols, rows, swz);
+  };
+  if (!in(&m[MAP_A], a, a_box) || !in(&m[MAP_B], b, b_box) || !out(&m[MAP_Y], j.Y, j.ldy)) return false;
+  m[MAP_A2] = m[MAP_A];
+  m[MAP_B2] = m[MAP_B];
+  m[MAP_Z] = m[MAP_Z2] = m[MAP_Y];
+  if (a2 && !in(&m[MAP_A2], *a2, a_box)) return false;
+  if (b2 && !in(&m[MAP_B2], *b2, b_box)) return false;
+  if (Z && !out(&m[MAP_Z], Z, j.N)) return false;
+  if (Z2 && !out(&m[MAP_Z2], Z2, j.N)) return false;
+  return !j.Y2 || out(&m[MAP_Y2], j.Y2, j.ldy);
 }
 
-Gemm16Params no_epilogue() {
-  Gemm16Params p = {};
-  p.act = SVDQ_EPI_NONE;
-  return p;
-}
-
-// out [M][N] = A B^T of row-major X [M][K] and W [N][K] (two weights: gated)
+// Y [M][N] = epilogue(X W^T) of row-major X [M][K] and W [N][K] (two weights: gated)
 svdq_status forward_product(const DeviceInfo& d, svdq_dtype dt, int M, int K, int N, const void* X, long long ldx,
-                            const void* W, const void* W2, Gemm16Params p, cudaStream_t stream) {
+                            const void* W, const void* W2, void* Y, long long ldy, Gemm16Params p,
+                            cudaStream_t stream) {
   const Gemm16Op op = W2 ? GEMM16_GATED : GEMM16_NT;
   const int nk = ceil_div(K, 64);
   const Operand x{X, (uint64_t)K, (uint64_t)M, (uint64_t)ldx}, w{W, (uint64_t)K, (uint64_t)N, (uint64_t)K},
       w2{W2, (uint64_t)K, (uint64_t)N, (uint64_t)K};
-  p.M = M;
-  p.N = N;
-  p.nk1 = p.nk = nk;
-  if (M <= SWAP_ROWS) {
-    const Gemm16Plan plan = plan_swap(op, M, N, nk, d.num_sms);
-    p.tiles_m = p.tiles_m1 = ceil_div(N, 128);
-    p.tiles_n = ceil_div(M, plan.bn);
-    return run_gemm(d, plan, dt, w, W2 ? &w2 : nullptr, x, nullptr, p, stream);
+  Gemm16Job& j = p.job[0];
+  j.M = M;
+  j.N = N;
+  j.nk1 = j.nk = nk;
+  j.Y = out16(Y);
+  j.ldy = ldy;
+  Gemm16Plan plan;
+  Gemm16Maps<2> maps;
+  bool ok;
+  const Choice pair = plan_pair(op, {ceil_div(M, 256), N, nk}, {}, d.num_sms);
+  const Choice swapped = M <= SWAP_ROWS ? plan_swap(op, M, N, nk, d.num_sms) : Choice{};
+  if (swapped.cycles > 0 && swapped.cycles < pair.cycles) {
+    plan = swapped.plan;
+    j.tiles_m = ceil_div(N, 128);
+    j.tiles_n = ceil_div(M, plan.bn);
+    ok = encode_job(plan, dt, w, W2 ? &w2 : nullptr, x, nullptr, j, p.Z, p.Z2, maps.m[0]);
+  } else {
+    plan = pair.plan;
+    j.tiles_m = ceil_div(M, 256);
+    j.tiles_n = ceil_div(N, W2 ? plan.bn / 2 : plan.bn);
+    ok = encode_job(plan, dt, x, nullptr, w, W2 ? &w2 : nullptr, j, p.Z, p.Z2, maps.m[0]);
   }
-  p.tiles_m = p.tiles_m1 = ceil_div(M, 256);
-  const Gemm16Plan plan = plan_pair(op, p.tiles_m, N, nk, d.num_sms);
-  p.tiles_n = ceil_div(N, W2 ? plan.bn / 2 : plan.bn);
-  return run_gemm(d, plan, dt, x, nullptr, w, W2 ? &w2 : nullptr, p, stream);
+  j.tiles_m1 = j.tiles_m;
+  if (!ok) return SVDQ_ERR_CUDA;
+  p.fp16 = dt == SVDQ_FP16;
+  p.err = d.err;
+  return cuda_status(launch_gemm16(plan, maps, p, d.num_sms, stream));
 }
 
-// dX [M][K] = dZ W (+ dZ2 W2), dZ [M][N] rows of stride ldz, W [N][K]
-svdq_status input_gradient(const DeviceInfo& d, svdq_dtype dt, int M, int K, int N, const void* dZ, long long ldz,
-                           const void* dZ2, const void* W, const void* W2, void* dX, long long lddx,
-                           cudaStream_t stream) {
-  const Operand z{dZ, (uint64_t)N, (uint64_t)M, (uint64_t)ldz}, z2{dZ2, (uint64_t)N, (uint64_t)M, (uint64_t)ldz},
-      w{W, (uint64_t)K, (uint64_t)N, (uint64_t)K}, w2{W2, (uint64_t)K, (uint64_t)N, (uint64_t)K};
-  Gemm16Params p = no_epilogue();
-  p.M = M;
-  p.N = K;
-  p.nk1 = ceil_div(N, 64);
-  p.nk = dZ2 ? 2 * p.nk1 : p.nk1;
-  p.Y = out16(dX);
-  p.ldy = lddx;
-  if (M <= SWAP_ROWS) {
-    const Gemm16Plan plan = plan_swap(GEMM16_NN, M, K, p.nk, d.num_sms);
-    p.tiles_m = p.tiles_m1 = ceil_div(K, 128);
-    p.tiles_n = ceil_div(M, plan.bn);
-    return run_gemm(d, plan, dt, w, dZ2 ? &w2 : nullptr, z, dZ2 ? &z2 : nullptr, p, stream);
+// The products of a backward pass, dZ (and dZ2) [M][N] of row stride ldz:
+//   dW [N][K] = dZ^T X, dW2 = dZ2^T X (stacked below it)   when dW
+//   dX [M][K] = dZ W + dZ2 W2                              when dX
+// and the bias gradients' sums (p.parts ...), in one launch.
+struct Backward {
+  int M, K, N;
+  const void *dZ, *dZ2, *X, *W, *W2;
+  long long ldz, ldx, lddx;
+  void *dX, *dW, *dW2;
+};
+svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward& g, Gemm16Params p,
+                              cudaStream_t stream) {
+  const uint64_t M = g.M, K = g.K, N = g.N, ldz = g.ldz;
+  const Operand z{g.dZ, N, M, ldz}, z2{g.dZ2, N, M, ldz}, w{g.W, K, N, K}, w2{g.W2, K, N, K},
+      x{g.X, K, M, (uint64_t)g.ldx};
+  const bool two = g.dZ2 != nullptr;
+  int jobs = 0, at_w = -1, at_x = -1;
+  JobShape shape[2] = {};
+  if (g.dW) {
+    at_w = jobs++;
+    Gemm16Job& j = p.job[at_w];
+    j.M = g.N;
+    j.N = g.K;
+    j.nk1 = j.nk = ceil_div(g.M, 64);
+    j.tiles_m1 = ceil_div(g.N, 256);
+    j.tiles_m = two ? 2 * j.tiles_m1 : j.tiles_m1;
+    j.a_mn = 1;
+    j.Y = out16(g.dW);
+    j.Y2 = out16(g.dW2);
+    j.ldy = g.K;
+    shape[at_w] = {j.tiles_m, g.K, j.nk};
   }
-  p.tiles_m = p.tiles_m1 = ceil_div(M, 256);
-  const Gemm16Plan plan = plan_pair(GEMM16_NN, p.tiles_m, K, p.nk, d.num_sms);
-  p.tiles_n = ceil_div(K, plan.bn);
-  return run_gemm(d, plan, dt, z, dZ2 ? &z2 : nullptr, w, dZ2 ? &w2 : nullptr, p, stream);
-}
-
-// dW [N][K] = dZ^T X (and dW2 = dZ2^T X, stacked below it as one launch)
-svdq_status weight_gradient(const DeviceInfo& d, svdq_dtype dt, int M, int K, int N, const void* dZ, long long ldz,
-                            const void* dZ2, const void* X, long long ldx, void* dW, void* dW2, cudaStream_t stream) {
-  const Operand z{dZ, (uint64_t)N, (uint64_t)M, (uint64_t)ldz}, z2{dZ2, (uint64_t)N, (uint64_t)M, (uint64_t)ldz},
-      x{X, (uint64_t)K, (uint64_t)M, (uint64_t)ldx};
-  Gemm16Params p = no_epilogue();
-  p.M = N;
-  p.N = K;
-  p.nk1 = p.nk = ceil_div(M, 64);
-  p.tiles_m1 = ceil_div(N, 256);
-  p.tiles_m = dZ2 ? 2 * p.tiles_m1 : p.tiles_m1;
-  p.Y = out16(dW);
-  p.Y2 = out16(dW2);
-  p.ldy = K;
-  const Gemm16Plan plan = plan_pair(GEMM16_TN, p.tiles_m, K, p.nk, d.num_sms);
-  p.tiles_n = ceil_div(K, plan.bn);
-  return run_gemm(d, plan, dt, z, dZ2 ? &z2 : nullptr, x, nullptr, p, stream);
+  if (g.dX) {
+    at_x = jobs++;
+    Gemm16Job& j = p.job[at_x];
+    j.M = g.M;
+    j.N = g.K;
+    j.nk1 = ceil_div(g.N, 64);
+    j.nk = two ? 2 * j.nk1 : j.nk1;
+    j.tiles_m = j.tiles_m1 = ceil_div(g.M, 256);
+    j.Y = out16(g.dX);
+    j.ldy = g.lddx;
+    shape[at_x] = {j.tiles_m, g.K, j.nk};
+  }
+  if (!jobs) return SVDQ_OK;
+  const Gemm16Plan plan = plan_pair(GEMM16_GRAD, shape[0], shape[1], d.num_sms).plan;
+  for (int i = 0; i < jobs; ++i) p.job[i].tiles_n = ceil_div(g.K, plan.bn);
+  if (jobs == 2 && p.job[1].nk > p.job[0].nk) {   // the longer tiles first
+    const Gemm16Job t = p.job[0];
+    p.job[0] = p.job[1];
+    p.job[1] = t;
+    at_w ^= 1;
+    at_x ^= 1;
+  }
+  Gemm16Maps<2> maps;
+  if (at_w >= 0 &&
+      !encode_job(plan, dt, z, two ? &z2 : nullptr, x, nullptr, p.job[at_w], nullptr, nullptr, maps.m[at_w]))
+    return SVDQ_ERR_CUDA;
+  if (at_x >= 0 && !encode_job(plan, dt, z, two ? &z2 : nullptr, w, two ? &w2 : nullptr, p.job[at_x], nullptr, nullptr,
+                               maps.m[at_x]))
+    return SVDQ_ERR_CUDA;
+  if (jobs == 1)
+    for (int i = 0; i < MAPS; ++i) maps.m[1][i] = maps.m[0][i];
+  p.fp16 = dt == SVDQ_FP16;
+  p.err = d.err;
+  return cuda_status(launch_gemm16(plan, maps, p, d.num_sms, stream));
 }
 
 cudaError_t zero(void* p, size_t bytes, cudaStream_t stream) {
@@ -203,15 +263,13 @@ svdq_status svdq_dense_linear(svdq_dtype dt, int M, int K, int N, const void* X,
   DeviceInfo d;
   const svdq_status s = current_device_info(&d);
   if (s != SVDQ_OK) return s;
-  Gemm16Params p = no_epilogue();
+  Gemm16Params p = {};
   p.act = act;
   p.bias = in16(bias);
   p.R = in16(residual);
   p.ldr = ldr;
-  p.Y = out16(Y);
-  p.ldy = ldy;
   p.Z = out16(Z);
-  return forward_product(d, dt, M, K, N, X, ldx, W_t, nullptr, p, stream);
+  return forward_product(d, dt, M, K, N, X, ldx, W_t, nullptr, Y, ldy, p, stream);
 }
 
 // [dZ when there is an activation | the bias gradient's partials]
@@ -244,7 +302,9 @@ svdq_status svdq_dense_linear_backward(svdq_dtype dt, int M, int K, int N, const
   const bool has_act = act != SVDQ_EPI_NONE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* part = reinterpret_cast<float*>(ws + (has_act ? align256((size_t)M * N * 2) : 0));
-  if (has_act || dbias) {
+  const bool products = dX || dW;
+  Gemm16Params q = {};
+  if ((has_act && products) || dbias) {
     ActGradParams p = {};
     p.kind = has_act ? ACT_GRAD_DENSE : ACT_GRAD_SUM;
     p.M = M;
@@ -258,15 +318,17 @@ svdq_status svdq_dense_linear_backward(svdq_dtype dt, int M, int K, int N, const
     p.part = dbias ? part : nullptr;
     p.parts = act_grad_parts(M, N);
     if ((s = cuda_status(launch_act_grad(p, stream))) != SVDQ_OK) return s;
-    if (dbias &&
-        (s = cuda_status(launch_sum_parts(part, p.parts, N, dt, dbias, nullptr, nullptr, stream))) != SVDQ_OK)
-      return s;
+    if (dbias) {
+      if (!products) return cuda_status(launch_sum_parts(part, p.parts, N, dt, dbias, nullptr, nullptr, stream));
+      q.parts = p.parts;
+      q.part_n = N;
+      q.part = part;
+      q.dbias = out16(dbias);
+    }
   }
   const void* dZ = has_act ? workspace : dY;
   const long long ldz = has_act ? N : lddy;
-  if (dX && (s = input_gradient(d, dt, M, K, N, dZ, ldz, nullptr, W_t, nullptr, dX, lddx, stream)) != SVDQ_OK)
-    return s;
-  return dW ? weight_gradient(d, dt, M, K, N, dZ, ldz, nullptr, X, ldx, dW, nullptr, stream) : SVDQ_OK;
+  return backward_products(d, dt, {M, K, N, dZ, nullptr, X, W_t, nullptr, ldz, ldx, lddx, dX, dW, nullptr}, q, stream);
 }
 
 // ------------------------------------------------------------------ gated feed-forward
@@ -282,15 +344,13 @@ svdq_status svdq_gated_linear(svdq_dtype dt, int M, int K, int F, const void* X,
   DeviceInfo d;
   const svdq_status s = current_device_info(&d);
   if (s != SVDQ_OK) return s;
-  Gemm16Params p = no_epilogue();
+  Gemm16Params p = {};
   p.act = act;
   p.bias = in16(bias_g);
   p.bias2 = in16(bias_u);
-  p.Y = out16(H);
-  p.ldy = ldh;
   p.Z = out16(G);
   p.Z2 = out16(U);
-  return forward_product(d, dt, M, K, F, X, ldx, Wg_t, Wu_t, p, stream);
+  return forward_product(d, dt, M, K, F, X, ldx, Wg_t, Wu_t, H, ldh, p, stream);
 }
 
 // [dG | dU | the two bias gradients' partials]
@@ -345,12 +405,19 @@ svdq_status svdq_gated_linear_backward(svdq_dtype dt, int M, int K, int F, const
   float* part2 = reinterpret_cast<float*>(ws + 2 * dz_bytes + align256((size_t)p.parts * F * 4));
   p.part = dbias_g ? part : nullptr;
   p.part2 = part2;
+  if (!dX && !dWg && !dbias_g) return SVDQ_OK;
   if ((s = cuda_status(launch_act_grad(p, stream))) != SVDQ_OK) return s;
-  if (dbias_g &&
-      (s = cuda_status(launch_sum_parts(part, p.parts, F, dt, dbias_g, part2, dbias_u, stream))) != SVDQ_OK)
-    return s;
-  if (dX && (s = input_gradient(d, dt, M, K, F, p.dZ, F, p.dU, Wg_t, Wu_t, dX, lddx, stream)) != SVDQ_OK) return s;
-  return dWg ? weight_gradient(d, dt, M, K, F, p.dZ, F, p.dU, X, ldx, dWg, dWu, stream) : SVDQ_OK;
+  if (!dX && !dWg) return cuda_status(launch_sum_parts(part, p.parts, F, dt, dbias_g, part2, dbias_u, stream));
+  Gemm16Params q = {};
+  if (dbias_g) {
+    q.parts = p.parts;
+    q.part_n = F;
+    q.part = part;
+    q.part2 = part2;
+    q.dbias = out16(dbias_g);
+    q.dbias2 = out16(dbias_u);
+  }
+  return backward_products(d, dt, {M, K, F, p.dZ, p.dU, X, Wg_t, Wu_t, F, ldx, lddx, dX, dWg, dWu}, q, stream);
 }
 
 // ------------------------------------------------------------------ layer norm

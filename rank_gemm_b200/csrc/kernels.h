@@ -241,35 +241,51 @@ size_t awq_smem_bytes(int K, int mb);
 
 // ---------------------------------------------------------------- 16-bit matrix products (gemm16.cu)
 // What is multiplied.  NT: both operands with the reduction index innermost
-// (X W^T).  NN: B with it outermost (dZ W).  TN: both outermost (dZ^T X).
-// GATED: NT with two weights and the gated epilogue.
-enum Gemm16Op { GEMM16_NT, GEMM16_GATED, GEMM16_NN, GEMM16_TN };
+// (X W^T).  GATED: NT with two weights and the gated epilogue.  GRAD: the
+// backward products, dZ^T X (both operands with the reduction index outermost)
+// and dZ W (B with it outermost), as the jobs of one launch.
+enum Gemm16Op { GEMM16_NT, GEMM16_GATED, GEMM16_GRAD };
 struct Gemm16Plan {
   Gemm16Op op;
   bool swap;     // the weight is the MMA's 128-row operand, the tokens its N
   int bn;        // MMA N: 128 or 256 (pair form), 16, 32, 64 or 128 (swapped)
-  int splits;    // CTAs (pairs) a tile's reduction is split over
+  int splits;    // CTAs (pairs) a tile's reduction is split over: a power of two
 };
-struct Gemm16Params {
-  int M, N;                    // rows and columns of the output
-  int tiles_m, tiles_n;        // tiles along the MMA's M and N
+struct Gemm16Job {
+  int M, N;                    // rows and columns of the output (of each of two stacked ones)
+  int tiles_m, tiles_n;        // tiles along the MMA's M and N; 0: no such job
   int tiles_m1;                // row blocks of the first of two stacked A operands (tiles_m: one)
   int nk1, nk;                 // 64-wide k-tiles of the first operand pair, of both
+  int group;                   // set by the launcher: row blocks of a group of tiles
+  int a_mn;                    // GRAD: A has the reduction index outermost
+  uint16_t *Y, *Y2;            // output rows of stride ldy; the second stacked output
+  long long ldy;
+};
+struct Gemm16Params {
+  Gemm16Job job[2];            // the second: GRAD only
   int splits;                  // set by the launcher
   int fp16;                    // 0 bf16, 1 fp16
+  // forward epilogue
   int act;                     // svdq_epilogue
   const uint16_t *bias, *bias2;
   const uint16_t* R;           // residual rows of stride ldr, or null
   long long ldr;
-  uint16_t *Y, *Y2;            // output rows of stride ldy; the second stacked output
-  long long ldy;
   uint16_t *Z, *Z2;            // pre-activations [M][N], or null
+  // GRAD: bias gradients from `parts` column-sum partials [parts][part_n] (0: none)
+  int parts, part_n;
+  const float *part, *part2;
+  uint16_t *dbias, *dbias2;
   DeviceErr err;
+};
+// A job's tensor maps; a map that nothing uses is a copy of another.
+enum Gemm16Map { MAP_A, MAP_A2, MAP_B, MAP_B2, MAP_Y, MAP_Z, MAP_Z2, MAPS, MAP_Y2 = MAP_Z2 };
+template <int JOBS>
+struct Gemm16Maps {
+  CUtensorMap m[JOBS][MAPS];
 };
 // Columns of the pair form's store boxes (32 rows high; 128-byte swizzle, 64-byte for 32 columns).
 constexpr int gemm16_box_cols(const Gemm16Plan& p) { return p.op == GEMM16_GATED && p.bn == 128 ? 32 : 64; }
-// Tensor maps: A, second A, B, second B; Y, Z, and Z2 or the second stacked output.
-cudaError_t launch_gemm16(const Gemm16Plan& plan, const CUtensorMap (&tm)[7], Gemm16Params p, int num_sms,
+cudaError_t launch_gemm16(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, Gemm16Params p, int num_sms,
                           cudaStream_t stream);
 
 // ---------------------------------------------------------------- column sums and activation slopes (act_grad.cu)
