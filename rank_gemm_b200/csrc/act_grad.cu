@@ -144,11 +144,12 @@ __global__ void __launch_bounds__(32 * SUM_LANES) sum_parts_kernel(const float* 
 
 }  // namespace
 
-// Row ranges: enough blocks for four a SM over the columns' blocks, at least
-// 16 rows each.
+// Row ranges: as many blocks as the SMs hold at four each and no more (a
+// second, nearly empty round cost 148 us instead of 103 for 4608 x 12288
+// gated), at least 16 rows each.
 int act_grad_parts(int M, int N) {
   const int cb = (N + COLS - 1) / COLS;
-  int parts = (148 * 4 + cb - 1) / cb;
+  int parts = 148 * 4 / cb;
   const int most = (M + 15) / 16;
   if (parts > most) parts = most;
   return parts < 1 ? 1 : parts;
