@@ -122,8 +122,10 @@ __device__ __forceinline__ bool all_warps_ok(bool ok) {
 __device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+// Relaxed: what it hands over, TMEM columns, has been read (tcgen05.wait::ld);
+// a release would wait for this thread's stores as well.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void tc_alloc(uint32_t dst_smem, uint32_t ncols) {
@@ -249,7 +251,7 @@ enum Out { OUT_Z, OUT_Z2, OUT_Y };   // which output a pass over the accumulator
 
 }  // namespace
 
-template <int CG, int BN, bool SWAP, bool GATED, bool GRAD>
+template <int CG, int BN, bool SWAP, bool GATED, bool GRAD, bool FP16>
 __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
     gemm16_kernel(const __grid_constant__ Gemm16Maps<GRAD ? 2 : 1> maps, const __grid_constant__ Gemm16Params p) {
   using C = Cfg<CG, BN, SWAP, GATED>;
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (the pair's first CTA)
     if (lane == 0 && cta == 0) {
-      const uint32_t idesc0 = (1u << 4) | (p.fp16 ? 0u : (1u << 7) | (1u << 10)) | (GRAD ? 1u << 16 : 0u) |
+      const uint32_t idesc0 = (1u << 4) | (FP16 ? 0u : (1u << 7) | (1u << 10)) | (GRAD ? 1u << 16 : 0u) |
                               ((uint32_t)(BN >> 3) << 17) | ((uint32_t)((128 * CG) >> 4) << 24);
       const uint16_t mask = (uint16_t)(3u << (rank & ~1u));
       auto commit = [&](uint64_t* bar) {
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
   // -------------------------------------------------------------- epilogue
   const int e = warp - 2, sub = warp & 3;
   const int row = sub * 32 + lane;                            // TMEM lane: row of this CTA's 128
-  const bool fp16 = p.fp16 != 0;
+  constexpr bool fp16 = FP16;
 
   if (GRAD && warp >= 2 && p.parts > 0) {
     // The bias gradients, 32 columns a block of CTAs: warp w adds parts w,
@@ -510,27 +512,33 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16) + ab * C::ACC_COLS;
       auto emit_box = [&](Out out, int at, int c) {
+        // the next 16 columns come out of TMEM while these are worked on
+        uint32_t r[2][16], q[2][GATED ? 16 : 1];
+        auto fetch = [&](int buf, int d) {
+          tmem_ld16(taddr + c + d, r[buf]);
+          if constexpr (GATED) tmem_ld16(taddr + BN / 2 + c + d, q[buf]);
+        };
+        fetch(0, 0);
         if (lane == 0) bulk_wait_read();   // the previous box has left shared memory
         __syncwarp();
-#pragma unroll 1
+#pragma unroll
         for (int d = 0; d < W; d += 16) {
-          uint32_t r[16], q[16];
-          tmem_ld16(taddr + c + d, r);
-          if (GATED) tmem_ld16(taddr + BN / 2 + c + d, q);
+          const int buf = (d >> 4) & 1;
           const uint4 now[2] = {res[0], res[1]};
           if (out == OUT_Y && c + d + 16 < c0 + PER) {
             res[0] = residual8(m, n_tile + c + d + 16);
             res[1] = residual8(m, n_tile + c + d + 24);
           }
           tmem_wait_ld();
+          if (d + 16 < W) fetch(buf ^ 1, d + 16);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float v[8], u[8];
             const int cc = c - c0 + d + 8 * h;   // column of the warp's
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              v[i] = __uint_as_float(r[8 * h + i]);
-              u[i] = GATED ? __uint_as_float(q[8 * h + i]) : 0.f;
+              v[i] = __uint_as_float(r[buf][8 * h + i]);
+              u[i] = GATED ? __uint_as_float(q[buf][GATED ? 8 * h + i : 0]) : 0.f;
             }
             if (!GRAD && p.bias) add_bias(v, GATED || cc < 64 ? bias_w[0] : bias_w[1], cc);
             if (GATED && p.bias2) add_bias(u, bias_w[1], cc);
@@ -721,10 +729,10 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
 
 namespace {
 
-template <int CG, int BN, bool SWAP, bool GATED, bool GRAD>
+template <int CG, int BN, bool SWAP, bool GATED, bool GRAD, bool FP16>
 cudaError_t launch(const Gemm16Maps<2>& maps, const Gemm16Params& p, int num_sms, cudaStream_t stream) {
   using C = Cfg<CG, BN, SWAP, GATED>;
-  auto kern = gemm16_kernel<CG, BN, SWAP, GATED, GRAD>;
+  auto kern = gemm16_kernel<CG, BN, SWAP, GATED, GRAD, FP16>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)p.job[0].tiles_m * p.job[0].tiles_n + (long long)p.job[1].tiles_m * p.job[1].tiles_n;
@@ -764,20 +772,16 @@ int group_rows(const Gemm16Job& j) {
   return (j.tiles_m + groups - 1) / groups;
 }
 
-}  // namespace
-
-cudaError_t launch_gemm16(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, Gemm16Params p, int num_sms,
-                          cudaStream_t stream) {
-  p.splits = plan.splits;
-  p.job[0].group = group_rows(p.job[0]);
-  p.job[1].group = group_rows(p.job[1]);
+template <bool FP16>
+cudaError_t launch_as(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, const Gemm16Params& p, int num_sms,
+                      cudaStream_t stream) {
   if (plan.swap) {
 #define SVDQ_SWAP(G)                                                                        \
   switch (plan.bn) {                                                                        \
-    case 16: return launch<1, 16, true, G, false>(maps, p, num_sms, stream);                \
-    case 32: return launch<1, 32, true, G, false>(maps, p, num_sms, stream);                \
-    case 64: return launch<1, 64, true, G, false>(maps, p, num_sms, stream);                \
-    case 128: return launch<1, 128, true, G, false>(maps, p, num_sms, stream);              \
+    case 16: return launch<1, 16, true, G, false, FP16>(maps, p, num_sms, stream);          \
+    case 32: return launch<1, 32, true, G, false, FP16>(maps, p, num_sms, stream);          \
+    case 64: return launch<1, 64, true, G, false, FP16>(maps, p, num_sms, stream);          \
+    case 128: return launch<1, 128, true, G, false, FP16>(maps, p, num_sms, stream);        \
     default: return cudaErrorInvalidValue;                                                  \
   }
     if (plan.op == GEMM16_NT) SVDQ_SWAP(false)
@@ -786,8 +790,8 @@ cudaError_t launch_gemm16(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, Gem
     return cudaErrorInvalidValue;
   }
 #define SVDQ_PAIR(G, B)                                                                     \
-  return plan.bn == 256 ? launch<2, 256, false, G, B>(maps, p, num_sms, stream)             \
-                        : launch<2, 128, false, G, B>(maps, p, num_sms, stream);
+  return plan.bn == 256 ? launch<2, 256, false, G, B, FP16>(maps, p, num_sms, stream)       \
+                        : launch<2, 128, false, G, B, FP16>(maps, p, num_sms, stream);
   switch (plan.op) {
     case GEMM16_NT: SVDQ_PAIR(false, false)
     case GEMM16_GATED: SVDQ_PAIR(true, false)
@@ -795,6 +799,16 @@ cudaError_t launch_gemm16(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, Gem
   }
 #undef SVDQ_PAIR
   return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_gemm16(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, Gemm16Params p, int num_sms,
+                          cudaStream_t stream) {
+  p.splits = plan.splits;
+  p.job[0].group = group_rows(p.job[0]);
+  p.job[1].group = group_rows(p.job[1]);
+  return p.fp16 ? launch_as<true>(plan, maps, p, num_sms, stream) : launch_as<false>(plan, maps, p, num_sms, stream);
 }
 
 }  // namespace svdq
