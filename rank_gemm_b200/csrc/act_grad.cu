@@ -55,6 +55,8 @@ __global__ void __launch_bounds__(THREADS) act_grad_kernel(ActGradParams p) {
   const int r0 = (int)((long long)p.M * blockIdx.y / gridDim.y), r1 = (int)((long long)p.M * (blockIdx.y + 1) / gridDim.y);
   const bool fp16 = p.fp16 != 0;
   float s[8] = {}, s2[8] = {};
+  grid_launch_dependents();   // the products' kernel may set up as SMs fall idle
+  grid_dependency_wait();
   if (n < p.N) {
 #pragma unroll 2
     for (int m = r0 + rl; m < r1; m += LANES) {
@@ -155,28 +157,34 @@ int act_grad_parts(int M, int N) {
   return parts < 1 ? 1 : parts;
 }
 
-cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream) {
-  const dim3 grid((p.N + COLS - 1) / COLS, p.parts);
-  switch (p.kind) {
-    case ACT_GRAD_SUM: act_grad_kernel<ACT_GRAD_SUM><<<grid, THREADS, 0, stream>>>(p); break;
-    case ACT_GRAD_DENSE: act_grad_kernel<ACT_GRAD_DENSE><<<grid, THREADS, 0, stream>>>(p); break;
-    case ACT_GRAD_GATED: act_grad_kernel<ACT_GRAD_GATED><<<grid, THREADS, 0, stream>>>(p); break;
-  }
-  return cudaGetLastError();
-}
-
-cudaError_t launch_sum_parts(const float* part, int parts, int N, int dt, void* out, const float* part2, void* out2,
-                             cudaStream_t stream) {
+// A launch that may be scheduled under the previous kernel's tail.
+template <typename... P, typename... A>
+static cudaError_t launch_early(void (*kern)(P...), dim3 grid, int block, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((N + 31) / 32, part2 ? 2 : 1);
-  cfg.blockDim = dim3(32 * SUM_LANES);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sum_parts_kernel, part, part2, parts, N, dt, out, out2);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream) {
+  const dim3 grid((p.N + COLS - 1) / COLS, p.parts);
+  switch (p.kind) {
+    case ACT_GRAD_SUM: return launch_early(act_grad_kernel<ACT_GRAD_SUM>, grid, THREADS, stream, p);
+    case ACT_GRAD_DENSE: return launch_early(act_grad_kernel<ACT_GRAD_DENSE>, grid, THREADS, stream, p);
+    default: return launch_early(act_grad_kernel<ACT_GRAD_GATED>, grid, THREADS, stream, p);
+  }
+}
+
+cudaError_t launch_sum_parts(const float* part, int parts, int N, int dt, void* out, const float* part2, void* out2,
+                             cudaStream_t stream) {
+  return launch_early(sum_parts_kernel, dim3((N + 31) / 32, part2 ? 2 : 1), 32 * SUM_LANES, stream, part, part2, parts, N,
+                      dt, out, out2);
 }
 
 }  // namespace svdq

@@ -69,10 +69,13 @@ Choice plan_pair(Gemm16Op op, JobShape a, JobShape b, int num_sms) {
     for (int s = 1; s <= 4; s *= 2) {
       const int slots = clusters(2 * s, num_sms);
       if (s > 1 && ((ta && a.nk < 4 * s) || (tb && b.nk < 4 * s) || tiles > slots)) break;
-      const int ka = ceil_div(a.nk, s), kb = ceil_div(b.nk, s), longest = ka > kb ? ka : kb;
-      // one job's tiles run in whole rounds; two jobs' even out, down to the longest tile
-      double k = tb ? ((double)ta * ka + (double)tb * kb) / slots : (double)((tiles + slots - 1) / slots) * ka;
-      if (k < longest) k = longest;
+      const int ka = ceil_div(a.nk, s), kb = ceil_div(b.nk, s);
+      // pair i takes tiles i, i + slots, ..., the first job's before the second's: the longest
+      // share is pair 0's, or that of the first pair with one tile fewer of the first job
+      const long long all = (tiles + slots - 1) / slots, a0 = (ta + slots - 1) / slots, p1 = ta % slots, a1 = ta / slots;
+      double k = (double)a0 * ka + (double)(all - a0) * kb;
+      const double k1 = (double)a1 * ka + (double)((tiles - p1 + slots - 1) / slots - a1) * kb;
+      if (p1 && k < k1) k = k1;
       best.offer({op, false, bn, s}, 9500 + k * per_k + (s > 1 ? exchange : 0));
     }
   }
@@ -218,15 +221,18 @@ svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward
     shape[at_x] = {j.tiles_m, g.K, j.nk};
   }
   if (!jobs) return SVDQ_OK;
-  const Gemm16Plan plan = plan_pair(GEMM16_GRAD, shape[0], shape[1], d.num_sms).plan;
-  for (int i = 0; i < jobs; ++i) p.job[i].tiles_n = ceil_div(g.K, plan.bn);
   if (jobs == 2 && p.job[1].nk > p.job[0].nk) {   // the longer tiles first
     const Gemm16Job t = p.job[0];
     p.job[0] = p.job[1];
     p.job[1] = t;
+    const JobShape u = shape[0];
+    shape[0] = shape[1];
+    shape[1] = u;
     at_w ^= 1;
     at_x ^= 1;
   }
+  const Gemm16Plan plan = plan_pair(GEMM16_GRAD, shape[0], shape[1], d.num_sms).plan;
+  for (int i = 0; i < jobs; ++i) p.job[i].tiles_n = ceil_div(g.K, plan.bn);
   Gemm16Maps<2> maps;
   if (at_w >= 0 &&
       !encode_job(plan, dt, z, two ? &z2 : nullptr, x, nullptr, p.job[at_w], nullptr, nullptr, maps.m[at_w]))
