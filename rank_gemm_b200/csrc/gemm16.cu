@@ -51,7 +51,7 @@ constexpr int SMEM_LIMIT = 232448;           // 227 KB
 constexpr int MAX_STAGES = 8;
 
 struct Ctl {
-  uint64_t full[MAX_STAGES], empty[MAX_STAGES], t_full[2], t_empty[2];
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES], t_full[2], t_empty[2], inbox;
   uint32_t tmem_base;
   int abort;
 };
@@ -70,12 +70,18 @@ struct Cfg {
   static constexpr int BOX_COLS = OUT_COLS / 2 < 64 ? OUT_COLS / 2 : 64;   // pair form: columns of a store box
   static constexpr int EPI_WARPS = SWAP ? 4 : 8;          // one or two per TMEM sub-partition
   static constexpr int PARK = SWAP ? BN * 256 : EPI_WARPS * 32 * BOX_COLS * 2;   // the store box, or one a warp
-  static constexpr int ROOM = (SMEM_LIMIT - 1024 - PARK - (int)sizeof(Ctl)) / STAGE;
-  static constexpr int STAGES = ROOM < MAX_STAGES ? ROOM : MAX_STAGES;
   static constexpr int ACC_COLS = A_TILES * BN;
+  // The partials a split tile's ranks send this one: memory of their own where
+  // five stages still fit beside it (the senders need not wait for this
+  // rank's MMAs then), else the ring.
+  static constexpr int INBOX_WANT = (ACC_COLS + 32 * A_TILES) * 512;
+  static constexpr int INBOX =
+      SWAP && (SMEM_LIMIT - 1024 - PARK - INBOX_WANT - (int)sizeof(Ctl)) / STAGE >= 5 ? INBOX_WANT : 0;
+  static constexpr int ROOM = (SMEM_LIMIT - 1024 - PARK - INBOX - (int)sizeof(Ctl)) / STAGE;
+  static constexpr int STAGES = ROOM < MAX_STAGES ? ROOM : MAX_STAGES;
   static constexpr int TMEM_COLS = pow2_at_least(2 * ACC_COLS, 32);
   static constexpr int THREADS = 32 * (2 + EPI_WARPS);
-  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + PARK + sizeof(Ctl);
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + PARK + INBOX + sizeof(Ctl);
   static_assert(STAGE % 1024 == 0, "tiles stay 1024-byte aligned for the 128-byte swizzle");
   static_assert(TMEM_COLS <= 512 && STAGES >= 3, "TMEM or ring too small");
   static_assert((ACC_COLS + 4 * A_TILES * 8) * 512 <= STAGES * STAGE, "a split's partial tile fits the ring");
@@ -164,6 +170,19 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b,
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// The same, counted on a barrier of the receiving CTA (16 bytes each).
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                            uint32_t cluster_bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(addr),
+      "r"(a), "r"(b), "r"(c), "r"(d), "r"(cluster_bar)
+      : "memory");
+}
+// cluster_sync_all that orders no memory: an arrival with release semantics
+// would wait for this thread's stores to global memory.
+__device__ __forceinline__ void cluster_sync_last() {
+  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+}
 __device__ __forceinline__ void st_dsmem_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -249,6 +268,13 @@ __device__ __forceinline__ void activate(float (&v)[COUNT], int act) {
 }
 enum Out { OUT_Z, OUT_Z2, OUT_Y };   // which output a pass over the accumulators makes
 
+// Token block of a tile of the swapped form.
+__device__ __forceinline__ int tile_tokens(const Gemm16Params& p, int tile) {
+  const Gemm16Job& j = p.job[0];
+  const int per = j.group * j.tiles_n, g = tile / per;
+  return (tile - g * per) / min(j.group, j.tiles_m - g * j.group);
+}
+
 }  // namespace
 
 template <int CG, int BN, bool SWAP, bool GATED, bool GRAD, bool FP16>
@@ -259,7 +285,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* park = ring + C::STAGES * C::STAGE;
-  Ctl* ctl = reinterpret_cast<Ctl*>(park + C::PARK);
+  Ctl* ctl = reinterpret_cast<Ctl*>(park + C::PARK + C::INBOX);
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -277,8 +303,14 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
       mbar_init(smem_u32(&ctl->t_full[s]), 1);
       mbar_init(smem_u32(&ctl->t_empty[s]), CG * C::EPI_WARPS);
     }
+    mbar_init(smem_u32(&ctl->inbox), 1);
     ctl->abort = 0;
     fence_barrier_init();
+    if (C::INBOX && S > 1) {   // the bytes the ranks will send: whole chunks of 16 columns up to the last token
+      const int own = OUT_COLS / S, tokens = p.job[0].M - tile_tokens(p, blockIdx.x / S) * BN;
+      const int cols = min(max(min((tokens + 15) / 16 * 16, BN) - split * own, 0), own);
+      mbar_arrive_expect_tx(smem_u32(&ctl->inbox), (uint32_t)(cols * 512 * S * C::A_TILES));
+    }
   }
   if (warp == 1) tc_alloc<CG>(smem_u32(&ctl->tmem_base), C::TMEM_COLS);
   tc_fence_before();
@@ -364,6 +396,14 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
             stage = 0;
             phase ^= 1;
           }
+        }
+      }
+      // the pair's commits have all arrived before this CTA may leave
+      for (int i = 0; CG == 2 && ok && i < C::STAGES; ++i) {
+        ok = mbar_wait(smem_u32(&ctl->empty[stage]), phase ^ 1, abort_flag, p.err);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
         }
       }
     }
@@ -561,7 +601,9 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(dsmem_map(smem_u32(&ctl->t_empty[ab]), rank & ~1u));
+      // not for a buffer no later tile waits for: nothing is left in flight towards the pair's first CTA
+      if (lane == 0 && tile + 2 * step < num_tiles)
+        mbar_arrive_cluster(dsmem_map(smem_u32(&ctl->t_empty[ab]), rank & ~1u));
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -642,7 +684,8 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
     constexpr int HALVES = GATED ? 2 : 1, HALF = C::ACC_COLS / HALVES;   // accumulator halves g and u
     constexpr int LOG_OUT = OUT_COLS == 256 ? 8 : OUT_COLS == 128 ? 7 : OUT_COLS == 64 ? 6 : OUT_COLS == 32 ? 5 : 4;
     const int log_own = LOG_OUT - (31 - __clz(S)), own = 1 << log_own;    // S is a power of two, own >= 4
-    const uint32_t line = (own + 4) * 4, inbox = smem_u32(ring) + row * line;
+    const uint32_t line = (own + 4) * 4;
+    const uint32_t inbox = smem_u32(C::INBOX ? park + C::PARK : ring) + row * line;
     const Tile t = tile_at(first);
     const Gemm16Job& j = p.job[t.job];
     bool ok = false;
@@ -650,7 +693,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
       ok = mbar_wait(smem_u32(&ctl->t_full[0]), 0, abort_flag, p.err);
       tc_fence_after();
     }
-    cluster_sync_all();
+    if (!C::INBOX) cluster_sync_all();
     if (warp >= 2 && ok) {
       const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16);
       for (int c = (e >> 2) * 16; c < C::ACC_COLS; c += 16 * (C::EPI_WARPS / 4)) {
@@ -663,12 +706,19 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const int q = (oc + i) >> log_own;
-          st_dsmem_v4(dsmem_map(slot + ((oc + i) & (own - 1)) * 4, q * CG + cta), r[i], r[i + 1], r[i + 2], r[i + 3]);
+          const uint32_t to = dsmem_map(slot + ((oc + i) & (own - 1)) * 4, q * CG + cta);
+          if (C::INBOX)
+            st_async_v4(to, r[i], r[i + 1], r[i + 2], r[i + 3], dsmem_map(smem_u32(&ctl->inbox), q));
+          else
+            st_dsmem_v4(to, r[i], r[i + 1], r[i + 2], r[i + 3]);
         }
       }
       tc_fence_before();
     }
-    cluster_sync_all();
+    if (!C::INBOX)
+      cluster_sync_all();
+    else if (warp >= 2)
+      ok = mbar_wait(smem_u32(&ctl->inbox), 0, abort_flag, p.err) && ok;
     // columns col .. col + 3 of the half
     auto total4 = [&](int half, int col, float* v) {
       const uint32_t from = inbox + half * 128 * line + col * 4;
@@ -717,7 +767,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
 
   tc_fence_before();
   if (CG * S > 1)
-    cluster_sync_all();   // no CTA leaves while another reads its shared memory or signals its barriers
+    cluster_sync_last();   // no CTA leaves while another reads its shared memory or signals its barriers
   else
     __syncthreads();
   if (warp == 1) {
