@@ -581,6 +581,18 @@ svdq_status svdq_layernorm_backward(svdq_dtype dt, int M, int C, const void* dY,
                                     cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * A W4A4 layer behind its layer norm (the pre-norm of a transformer block):
+ * svdq_layernorm on the packed bf16 rows X [M][K] (gamma, beta [K] or both
+ * NULL) into the workspace, then svdq_linear on those rows; the same bits as
+ * the two calls.  Workspace: svdq_norm_linear_workspace_bytes (the normalized
+ * rows, then svdq_linear's).  Errors: those of the two calls.
+ * ------------------------------------------------------------------------ */
+size_t svdq_norm_linear_workspace_bytes(const svdq_weights* w, int M);
+svdq_status svdq_norm_linear(const svdq_weights* w, int M, const void* X, const void* gamma, const void* beta,
+                             float eps, svdq_epilogue epi, void* Y, void* workspace, size_t ws_bytes,
+                             cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Diagnostics.
  * svdq_poll_device_error: synchronizes `stream`, then reads and clears the
  *   current device's error word.  Returns SVDQ_OK, SVDQ_ERR_TIMEOUT (a wait

@@ -102,6 +102,8 @@ _SIGS = {
     "svdq_layernorm": (_i, [_i, _i, _i, _vp, _ll, _vp, _vp, _f, _vp, _ll, _vp, _vp, _vp]),
     "svdq_layernorm_backward_workspace_bytes": (_sz, [_i, _i]),
     "svdq_layernorm_backward": (_i, [_i, _i, _i, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _ll, _vp, _vp, _vp, _sz, _vp]),
+    "svdq_norm_linear_workspace_bytes": (_sz, [_vp, _i]),
+    "svdq_norm_linear": (_i, [_vp, _i, _vp, _vp, _vp, _f, _i, _vp, _vp, _sz, _vp]),
     "svdq_poll_device_error": (_i, [_vp]),
     "svdq_selftest_wait_timeout": (_i, [ctypes.c_uint, _vp]),
     "svdq_debug_override_cc": (None, [_i, _i]),
@@ -448,6 +450,16 @@ def svdq_layernorm_backward(M, C, dY, X, gamma, mean, rstd, dX, dgamma, dbeta, w
                                        _flat(rstd, M, torch.float32, dev, "rstd"), dx, lddx,
                                        _flat(dgamma, C, dt, dev, "dgamma"), _flat(dbeta, C, dt, dev, "dbeta"), ws,
                                        ws_bytes, _stream(stream)), "svdq_layernorm_backward")
+
+
+def svdq_norm_linear_workspace_bytes(w, M) -> int:
+    return lib.svdq_norm_linear_workspace_bytes(w, M)
+
+
+def svdq_norm_linear(w, M, X, gamma, beta, eps, epi, Y, workspace, ws_bytes=None, stream=None):
+    ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
+    _check(lib.svdq_norm_linear(w, M, _ptr(X), _ptr(gamma), _ptr(beta), eps, epi, _ptr(Y), _ptr(workspace), ws_bytes,
+                                _stream(stream)), "svdq_norm_linear")
 
 
 def svdq_poll_device_error(stream=None) -> int:

@@ -485,4 +485,33 @@ svdq_status svdq_layernorm_backward(svdq_dtype dt, int M, int C, const void* dY,
   return cuda_status(launch_sum_parts(pg, parts, C, dt, dgamma, pb, dbeta, stream));
 }
 
+// ------------------------------------------------------------------ a W4A4 layer behind its norm
+static size_t normed_bytes(const svdq_weights_info& i, int M) { return align256((size_t)M * i.K * 2); }
+
+size_t svdq_norm_linear_workspace_bytes(const svdq_weights* w, int M) {
+  svdq_weights_info i;
+  if (M < 0 || svdq_weights_view(w, &i) != SVDQ_OK) return 0;
+  return normed_bytes(i, M) + svdq_linear_workspace_bytes(w, M);
+}
+
+svdq_status svdq_norm_linear(const svdq_weights* w, int M, const void* X, const void* gamma, const void* beta,
+                             float eps, svdq_epilogue epi, void* Y, void* workspace, size_t ws_bytes,
+                             cudaStream_t stream) {
+  svdq_weights_info i;
+  if (svdq_weights_view(w, &i) != SVDQ_OK || (M > 0 && (!X || !Y))) return SVDQ_ERR_INVALID_ARG;
+  if (epi != SVDQ_EPI_NONE && epi != SVDQ_EPI_GELU_TANH) return SVDQ_ERR_INVALID_ARG;
+  if (!gamma != !beta || !(eps >= 0.f) || !std::isfinite(eps)) return SVDQ_ERR_INVALID_ARG;
+  if (M < 0) return SVDQ_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(gamma) || !aligned16(beta) || (reinterpret_cast<uintptr_t>(Y) & 31u))
+    return SVDQ_ERR_ALIGNMENT;
+  if (M == 0) return SVDQ_OK;
+  if (!workspace || ws_bytes < svdq_norm_linear_workspace_bytes(w, M)) return SVDQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return SVDQ_ERR_ALIGNMENT;
+  svdq_status s = handle_device_status(w);
+  if (s != SVDQ_OK) return s;
+  uint8_t* rest = static_cast<uint8_t*>(workspace) + normed_bytes(i, M);
+  s = svdq_layernorm(SVDQ_BF16, M, i.K, X, i.K, gamma, beta, eps, workspace, i.K, nullptr, nullptr, stream);
+  return s != SVDQ_OK ? s : svdq_linear(w, M, workspace, epi, Y, rest, ws_bytes - normed_bytes(i, M), stream);
+}
+
 }  // extern "C"

@@ -101,6 +101,11 @@ def test_good_calls_reach_the_device_check(B):
     assert call(B, "svdq_layernorm_backward", dgamma=None, dbeta=None, workspace=None, ws_bytes=0) == UNSUPPORTED
 
 
+def test_norm_linear_refuses_a_null_handle(B):
+    assert B.lib.svdq_norm_linear(None, 4, P, P, P, 1e-5, 0, P, P, BIG, None) == INVALID
+    assert B.lib.svdq_norm_linear_workspace_bytes(None, 4) == 0
+
+
 def test_workspace_sizes(B):
     L = B.lib
     assert L.svdq_dense_linear_backward_workspace_bytes(-1, 64, 64, 0) == 0
