@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "svdq.h"
@@ -57,26 +58,48 @@ struct Choice {
   }
 };
 struct JobShape {
-  int rows, cols, nk;   // row blocks of 256, columns, k-tiles
+  int M, N, nk;        // output rows and columns, k-tiles
+  int stacked;         // outputs stacked along the rows
 };
+// The longest share of a pair, in cycles (ca, cb a tile), as the kernel deals
+// the tiles out: `per` tiles of the second job make up for one of the first.
+long long longest_share(long long ta, long long ca, long long tb, long long cb, int per, int slots) {
+  const long long r = ta % slots, few = slots - r;
+  const long long extra = tb && r ? std::min(tb, per * few) : 0, rest = tb - extra;
+  long long most = 0;
+  const long long at[4] = {0, r > 0 ? r - 1 : 0, r, slots - 1};   // the shares step at these pairs
+  for (long long p : at) {
+    const long long n0 = ta / slots + (p < r), n1 = p >= r && extra > p - r ? (extra - (p - r) + few - 1) / few : 0;
+    const long long q = slots - 1 - p, n2 = rest > q ? (rest - q + slots - 1) / slots : 0;
+    most = std::max(most, n0 * ca + (n1 + n2) * cb);
+  }
+  return most;
+}
 Choice plan_pair(Gemm16Op op, JobShape a, JobShape b, int num_sms) {
   Choice best;
-  for (int bn = 256; bn >= 128; bn -= 128) {
-    const int out_cols = op == GEMM16_GATED ? bn / 2 : bn;
-    const double per_k = bn == 256 ? 620 : 480, exchange = bn == 256 ? 12000 : 5000;
-    const long long ta = (long long)a.rows * ceil_div(a.cols, out_cols),
-                    tb = (long long)b.rows * ceil_div(b.cols, out_cols), tiles = ta + tb;
-    for (int s = 1; s <= 4; s *= 2) {
+  struct Form {
+    int rows, bn, k_tile, tile, exchange;
+    bool tall;
+  };
+  // Cycles of a k-tile, of a tile besides, of a split's exchange.  512 x 256
+  // tiles take 0.94 of the time of two 256 x 256 at 128 k-tiles (8192^3: 826
+  // us, 875), 0.96 at 72 and 1.01 at 48, and leave more pairs idle at the end.
+  const Form forms[3] = {{512, 256, 1130, 6000, 0, true}, {256, 256, 620, 0, 12000, false},
+                         {256, 128, 480, 0, 5000, false}};
+  for (const Form& f : forms) {
+    if (f.tall && op == GEMM16_GATED) continue;
+    const int out_cols = op == GEMM16_GATED ? f.bn / 2 : f.bn;
+    auto tiles_of = [&](const JobShape& j) {
+      return j.nk ? (long long)j.stacked * ceil_div(j.M, f.rows) * ceil_div(j.N, out_cols) : 0;
+    };
+    const long long ta = tiles_of(a), tb = tiles_of(b), tiles = ta + tb;
+    for (int s = 1; s <= (f.tall ? 1 : 4); s *= 2) {
       const int slots = clusters(2 * s, num_sms);
       if (s > 1 && ((ta && a.nk < 4 * s) || (tb && b.nk < 4 * s) || tiles > slots)) break;
-      const int ka = ceil_div(a.nk, s), kb = ceil_div(b.nk, s);
-      // pair i takes tiles i, i + slots, ..., the first job's before the second's: the longest
-      // share is pair 0's, or that of the first pair with one tile fewer of the first job
-      const long long all = (tiles + slots - 1) / slots, a0 = (ta + slots - 1) / slots, p1 = ta % slots, a1 = ta / slots;
-      double k = (double)a0 * ka + (double)(all - a0) * kb;
-      const double k1 = (double)a1 * ka + (double)((tiles - p1 + slots - 1) / slots - a1) * kb;
-      if (p1 && k < k1) k = k1;
-      best.offer({op, false, bn, s}, 9500 + k * per_k + (s > 1 ? exchange : 0));
+      const long long share = longest_share(ta, (long long)ceil_div(a.nk, s) * f.k_tile + f.tile, tb,
+                                            (long long)ceil_div(b.nk, s) * f.k_tile + f.tile,
+                                            gemm16_extra(a.nk, b.nk), slots);
+      best.offer({op, false, f.bn, s, f.tall}, 9500 + (double)share + (s > 1 ? f.exchange : 0));
     }
   }
   return best;
@@ -93,7 +116,7 @@ Choice plan_swap(Gemm16Op op, int tokens, int features, int nk, int num_sms) {
       if (s > 1 && (nk < 2 * s || tiles > slots)) break;
       double t = (double)((tiles + slots - 1) / slots) * ceil_div(nk, s) * per_k;
       if (t < stream) t = stream;
-      best.offer({op, true, bn, s}, 8500 + t + 15 * bn + (s > 1 ? 1500 + 45 * bn : 0));
+      best.offer({op, true, bn, s, false}, 8500 + t + 15 * bn + (s > 1 ? 1500 + 45 * bn : 0));
     }
     if (bn >= tokens) break;
   }
@@ -156,7 +179,7 @@ svdq_status forward_product(const DeviceInfo& d, svdq_dtype dt, int M, int K, in
   Gemm16Plan plan;
   Gemm16Maps<2> maps;
   bool ok;
-  const Choice pair = plan_pair(op, {ceil_div(M, 256), N, nk}, {}, d.num_sms);
+  const Choice pair = plan_pair(op, {M, N, nk, 1}, {}, d.num_sms);
   const Choice swapped = M <= SWAP_ROWS ? plan_swap(op, M, N, nk, d.num_sms) : Choice{};
   if (swapped.cycles > 0 && swapped.cycles < pair.cycles) {
     plan = swapped.plan;
@@ -165,7 +188,7 @@ svdq_status forward_product(const DeviceInfo& d, svdq_dtype dt, int M, int K, in
     ok = encode_job(plan, dt, w, W2 ? &w2 : nullptr, x, nullptr, j, p.Z, p.Z2, maps.m[0]);
   } else {
     plan = pair.plan;
-    j.tiles_m = ceil_div(M, 256);
+    j.tiles_m = ceil_div(M, plan.tall ? 512 : 256);
     j.tiles_n = ceil_div(N, W2 ? plan.bn / 2 : plan.bn);
     ok = encode_job(plan, dt, x, nullptr, w, W2 ? &w2 : nullptr, j, p.Z, p.Z2, maps.m[0]);
   }
@@ -200,13 +223,11 @@ svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward
     j.M = g.N;
     j.N = g.K;
     j.nk1 = j.nk = ceil_div(g.M, 64);
-    j.tiles_m1 = ceil_div(g.N, 256);
-    j.tiles_m = two ? 2 * j.tiles_m1 : j.tiles_m1;
     j.a_mn = 1;
     j.Y = out16(g.dW);
     j.Y2 = out16(g.dW2);
     j.ldy = g.K;
-    shape[at_w] = {j.tiles_m, g.K, j.nk};
+    shape[at_w] = {g.N, g.K, j.nk, two ? 2 : 1};
   }
   if (g.dX) {
     at_x = jobs++;
@@ -215,10 +236,9 @@ svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward
     j.N = g.K;
     j.nk1 = ceil_div(g.N, 64);
     j.nk = two ? 2 * j.nk1 : j.nk1;
-    j.tiles_m = j.tiles_m1 = ceil_div(g.M, 256);
     j.Y = out16(g.dX);
     j.ldy = g.lddx;
-    shape[at_x] = {j.tiles_m, g.K, j.nk};
+    shape[at_x] = {g.M, g.K, j.nk, 1};
   }
   if (!jobs) return SVDQ_OK;
   if (jobs == 2 && p.job[1].nk > p.job[0].nk) {   // the longer tiles first
@@ -232,7 +252,11 @@ svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward
     at_x ^= 1;
   }
   const Gemm16Plan plan = plan_pair(GEMM16_GRAD, shape[0], shape[1], d.num_sms).plan;
-  for (int i = 0; i < jobs; ++i) p.job[i].tiles_n = ceil_div(g.K, plan.bn);
+  for (int i = 0; i < jobs; ++i) {
+    p.job[i].tiles_n = ceil_div(g.K, plan.bn);
+    p.job[i].tiles_m1 = ceil_div(shape[i].M, plan.tall ? 512 : 256);
+    p.job[i].tiles_m = shape[i].stacked * p.job[i].tiles_m1;
+  }
   Gemm16Maps<2> maps;
   if (at_w >= 0 &&
       !encode_job(plan, dt, z, two ? &z2 : nullptr, x, nullptr, p.job[at_w], nullptr, nullptr, maps.m[at_w]))

@@ -17,6 +17,12 @@
 //                         fetched into shared memory once per pair; the two
 //                         float32 accumulators of TMEM alternate, so the
 //                         epilogue of one tile runs under the next one's MMAs.
+//   tall pair (TALL)      a 512 x 256 tile, two 256-row accumulators over the
+//                         same B: a quarter less operand traffic per product.
+//                         TMEM holds no second pair of accumulators, so the
+//                         first and last k-tiles run for one accumulator and
+//                         then for the other, while the epilogue drains or
+//                         has drained the other one.
 //   swapped form (SWAP)   for few rows of X (tokens): the weight is the
 //                         128-row operand and the tokens are the MMA's N
 //                         (16 .. 128), so a token batch does not fill a
@@ -58,9 +64,10 @@ struct Ctl {
 
 constexpr int pow2_at_least(int x, int lo) { return x <= lo ? lo : pow2_at_least(x, 2 * lo); }
 
-template <int CG, int BN, bool SWAP, bool GATED>
+template <int CG, int BN, bool SWAP, bool GATED, bool TALL>
 struct Cfg {
-  static constexpr int A_TILES = (SWAP && GATED) ? 2 : 1;
+  static constexpr int A_TILES = (SWAP && GATED) || TALL ? 2 : 1;
+  static constexpr int TILE_ROWS = 128 * CG * (TALL ? 2 : 1);   // along the MMA's M
   static constexpr int A_TILE_BYTES = 128 * BK * 2;
   static constexpr int A_BYTES = A_TILES * A_TILE_BYTES;
   static constexpr int B_ROWS = BN / CG;                  // per CTA
@@ -79,12 +86,12 @@ struct Cfg {
       SWAP && (SMEM_LIMIT - 1024 - PARK - INBOX_WANT - (int)sizeof(Ctl)) / STAGE >= 5 ? INBOX_WANT : 0;
   static constexpr int ROOM = (SMEM_LIMIT - 1024 - PARK - INBOX - (int)sizeof(Ctl)) / STAGE;
   static constexpr int STAGES = ROOM < MAX_STAGES ? ROOM : MAX_STAGES;
-  static constexpr int TMEM_COLS = pow2_at_least(2 * ACC_COLS, 32);
+  static constexpr int TMEM_COLS = TALL ? ACC_COLS : pow2_at_least(2 * ACC_COLS, 32);
   static constexpr int THREADS = 32 * (2 + EPI_WARPS);
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + PARK + INBOX + sizeof(Ctl);
   static_assert(STAGE % 1024 == 0, "tiles stay 1024-byte aligned for the 128-byte swizzle");
   static_assert(TMEM_COLS <= 512 && STAGES >= 3, "TMEM or ring too small");
-  static_assert((ACC_COLS + 4 * A_TILES * 8) * 512 <= STAGES * STAGE, "a split's partial tile fits the ring");
+  static_assert(TALL || (ACC_COLS + 4 * A_TILES * 8) * 512 <= STAGES * STAGE, "a split's partial tile fits the ring");
 };
 
 // ------------------------------------------------------------------ PTX forms this kernel adds
@@ -277,10 +284,10 @@ __device__ __forceinline__ int tile_tokens(const Gemm16Params& p, int tile) {
 
 }  // namespace
 
-template <int CG, int BN, bool SWAP, bool GATED, bool GRAD, bool FP16>
-__global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
+template <int CG, int BN, bool SWAP, bool GATED, bool GRAD, bool TALL, bool FP16>
+__global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
     gemm16_kernel(const __grid_constant__ Gemm16Maps<GRAD ? 2 : 1> maps, const __grid_constant__ Gemm16Params p) {
-  using C = Cfg<CG, BN, SWAP, GATED>;
+  using C = Cfg<CG, BN, SWAP, GATED, TALL>;
   constexpr int OUT_COLS = C::OUT_COLS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -325,26 +332,40 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
   grid_launch_dependents();
   if (warp != 1) grid_dependency_wait();
 
-  const int tiles0 = p.job[0].tiles_m * p.job[0].tiles_n;
-  const int num_tiles = tiles0 + (GRAD ? p.job[1].tiles_m * p.job[1].tiles_n : 0);
-  const int first = (int)blockIdx.x / (CG * S), step = (int)gridDim.x / (CG * S);
-  // Tile -> job and block coordinates.  Tiles run down groups of row blocks,
-  // so the tiles in flight share rows of A and columns of B in L2.
+  const int first = (int)blockIdx.x / (CG * S), slots = (int)gridDim.x / (CG * S);   // this pair (CTA, cluster), of how many
+  const int tiles0 = p.job[0].tiles_m * p.job[0].tiles_n, tiles1 = GRAD ? p.job[1].tiles_m * p.job[1].tiles_n : 0;
+  // The n-th tile of this pair: its job and block coordinates.  Job 0's tiles
+  // go round the pairs; the pairs left with one fewer of them take
+  // job1_extra tiles of job 1 each, and the rest of job 1 goes round from the
+  // last pair.  Within a job tiles run down groups of row blocks, so the tiles
+  // in flight share rows of A and columns of B in L2.
   struct Tile {
+    bool valid;
     int job, mb, nb;
     bool second;   // of two stacked A operands and outputs; mb counts within it
   };
-  auto tile_at = [&](int tile) {
+  auto tile_at = [&](int n) {
     Tile t;
-    t.job = GRAD && tile >= tiles0;
-    const Gemm16Job& j = p.job[t.job];
-    if (t.job) tile -= tiles0;
-    const int per = j.group * j.tiles_n, g = tile / per, r = tile - g * per;
-    const int rows = min(j.group, j.tiles_m - g * j.group);
-    t.mb = g * j.group + r % rows;
-    t.nb = r / rows;
-    t.second = t.mb >= j.tiles_m1;
-    if (t.second) t.mb -= j.tiles_m1;
+    int tile = first + n * slots;
+    t.job = 0;
+    t.valid = tile < tiles0;
+    if (GRAD && !t.valid && tiles1 > 0) {
+      const int r = tiles0 % slots, few = slots - r, n1 = n - (tiles0 / slots + (first < r));
+      const int extra = r ? min(tiles1, p.job1_extra * few) : 0;
+      const int mine = first >= r && extra > 0 ? (extra - (first - r) + few - 1) / few : 0;
+      tile = n1 < mine ? first - r + n1 * few : extra + (slots - 1 - first) + (n1 - mine) * slots;
+      t.job = 1;
+      t.valid = tile < tiles1;
+    }
+    if (t.valid) {
+      const Gemm16Job& j = p.job[t.job];
+      const int per = j.group * j.tiles_n, g = tile / per, q = tile - g * per;
+      const int rows = min(j.group, j.tiles_m - g * j.group);
+      t.mb = g * j.group + q % rows;
+      t.nb = q / rows;
+      t.second = t.mb >= j.tiles_m1;
+      if (t.second) t.mb -= j.tiles_m1;
+    }
     return t;
   };
   auto k_begin = [&](const Gemm16Job& j) { return (int)((long long)j.nk * split / S); };
@@ -356,12 +377,13 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = first; ok && tile < num_tiles; tile += step) {
-        const Tile t = tile_at(tile);
+      for (int n = 0; ok; ++n) {
+        const Tile t = tile_at(n);
+        if (!t.valid) break;
         const Gemm16Job& j = p.job[t.job];
         const CUtensorMap* map = maps.m[t.job];
         const bool a_mn = GRAD && j.a_mn;
-        const int a_row = t.mb * 128 * CG + cta * 128;
+        const int a_row = t.mb * C::TILE_ROWS + cta * 128;
         const int b_row = (GATED && !SWAP) ? t.nb * OUT_COLS : t.nb * BN + cta * C::B_ROWS;
         const int kt1 = k_end(j);
         for (int kt = k_begin(j); kt < kt1; ++kt) {
@@ -388,8 +410,10 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
               for (int i = 0; i < rows; i += 64) load(dst + i * 128, m, row + i, k);
             }
           };
-          load_tile(a, map + (t.second || seg ? MAP_A2 : MAP_A), a_mn, 128, a_row);
-          if (C::A_TILES == 2) load_tile(a + C::A_TILE_BYTES, map + MAP_A2, false, 128, a_row);
+          const CUtensorMap* map_a = map + (t.second || seg ? MAP_A2 : MAP_A);
+          load_tile(a, map_a, a_mn, 128, a_row);
+          if (TALL) load_tile(a + C::A_TILE_BYTES, map_a, a_mn, 128, a_row + 256);
+          if (SWAP && GATED) load_tile(a + C::A_TILE_BYTES, map + MAP_A2, false, 128, a_row);
           const bool b2 = (GATED && !SWAP) ? cta == 1 : seg;
           load_tile(b, map + (b2 ? MAP_B2 : MAP_B), GRAD, C::B_ROWS, b_row);
           if (++stage == C::STAGES) {
@@ -419,41 +443,85 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
         else
           tc_commit(smem_u32(bar));
       };
-      int stage = 0;
-      uint32_t phase = 0, tl = 0;
-      bool ok = true;
-      for (int tile = first; ok && tile < num_tiles; tile += step, ++tl) {
-        const Gemm16Job& job = p.job[GRAD && tile >= tiles0];
-        const bool a_mn = GRAD && job.a_mn;
-        const uint32_t idesc = idesc0 | (a_mn ? 1u << 15 : 0u);
-        const uint32_t ab = tl & 1, pt = (tl >> 1) & 1;
-        if (!mbar_wait(smem_u32(&ctl->t_empty[ab]), pt ^ 1, abort_flag, p.err)) break;
-        tc_fence_after();
-        const uint32_t acc = tmem + ab * C::ACC_COLS;
-        const int kt0 = k_begin(job), kt1 = k_end(job);
-        for (int kt = kt0; kt < kt1; ++kt) {
-          if (!mbar_wait(smem_u32(&ctl->full[stage]), phase, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a = smem_u32(ring + stage * C::STAGE), b = a + C::A_BYTES;
-#pragma unroll
-          for (int j = 0; j < BK / 16; ++j) {
-            const uint64_t db = operand_desc(GRAD, b, j);
-#pragma unroll
-            for (int t = 0; t < C::A_TILES; ++t)
-              mma_f16<CG>(acc + t * BN, operand_desc(a_mn, a + t * C::A_TILE_BYTES, j), db, idesc,
-                          kt != kt0 || j != 0);
-          }
-          commit(&ctl->empty[stage]);
+      // a place in the ring
+      struct Slot {
+        int stage;
+        uint32_t phase;
+        __device__ void next() {
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (!ok) break;
-        commit(&ctl->t_full[ab]);
+      };
+      Slot at{0, 0};
+      auto filled = [&](const Slot& x) {
+        const bool ok = mbar_wait(smem_u32(&ctl->full[x.stage]), x.phase, abort_flag, p.err);
+        tc_fence_after();
+        return ok;
+      };
+      uint32_t idesc = idesc0;
+      bool a_mn = false;
+      // one k-tile into the accumulators [t0, t1) of the tile at column acc
+      auto multiply = [&](const Slot& x, uint32_t acc, int t0, int t1, bool first_k) {
+        const uint32_t a = smem_u32(ring + x.stage * C::STAGE), b = a + C::A_BYTES;
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k) {
+          const uint64_t db = operand_desc(GRAD, b, k);
+#pragma unroll
+          for (int t = 0; t < C::A_TILES; ++t)
+            if (t >= t0 && t < t1)
+              mma_f16<CG>(acc + t * BN, operand_desc(a_mn, a + t * C::A_TILE_BYTES, k), db, idesc, !first_k || k != 0);
+        }
+      };
+      auto drained = [&](int buf, uint32_t use) {
+        const bool ok = mbar_wait(smem_u32(&ctl->t_empty[buf]), (use & 1) ^ 1, abort_flag, p.err);
+        tc_fence_after();
+        return ok;
+      };
+      bool ok = true;
+      for (uint32_t n = 0; ok; ++n) {
+        const Tile tile = tile_at((int)n);
+        if (!tile.valid) break;
+        const Gemm16Job& job = p.job[tile.job];
+        a_mn = GRAD && job.a_mn;
+        idesc = idesc0 | (a_mn ? 1u << 15 : 0u);
+        const int nk = k_end(job) - k_begin(job);
+        if (!TALL) {
+          const uint32_t ab = n & 1;
+          ok = drained(ab, n >> 1);
+          for (int k = 0; ok && k < nk; ++k, at.next()) {
+            if (!(ok = filled(at))) break;
+            multiply(at, tmem + ab * C::ACC_COLS, 0, C::A_TILES, k == 0);
+            commit(&ctl->empty[at.stage]);
+          }
+          if (ok) commit(&ctl->t_full[ab]);
+        } else {
+          // k-tiles [k0, k1), at most a ring of them: accumulator 0, then 1 and their release
+          auto apart = [&](int k0, int k1, bool last) {
+            Slot x = at;
+            for (int k = k0; k < k1; ++k, x.next()) {
+              if (!filled(x)) return false;
+              multiply(x, tmem, 0, 1, k == 0);
+            }
+            if (last) commit(&ctl->t_full[0]);
+            if (k0 == 0 && !drained(1, n)) return false;
+            for (int k = k0; k < k1; ++k, at.next()) {
+              multiply(at, tmem, 1, 2, k == 0);
+              commit(&ctl->empty[at.stage]);
+            }
+            if (last) commit(&ctl->t_full[1]);
+            return true;
+          };
+          const int head = min(nk, C::STAGES), tail = min(nk - head, C::STAGES);
+          ok = drained(0, n) && apart(0, head, nk == head);
+          for (int k = head; ok && k < nk - tail; ++k, at.next()) {
+            if (!(ok = filled(at))) break;
+            multiply(at, tmem, 0, 2, false);
+            commit(&ctl->empty[at.stage]);
+          }
+          if (ok && tail) ok = apart(nk - tail, nk, true);
+        }
       }
     }
   }
@@ -520,22 +588,25 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
     constexpr int PER = OUT_COLS / 2, W = C::BOX_COLS;
     const int c0 = (e >> 2) * PER;
     const uint32_t box = smem_u32(park) + (uint32_t)e * (32 * W * 2);
-    uint32_t tl = 0;
-    for (int tile = first; tile < num_tiles; tile += step, ++tl) {
-      const Tile t = tile_at(tile);
+    // n counts accumulators: one a tile, or two (TALL)
+    constexpr int PARTS = TALL ? 2 : 1;
+    Tile t = tile_at(0);
+    for (int n = 0; t.valid; ++n) {
+      const int part = n % PARTS;
       const Gemm16Job& j = p.job[t.job];
       const CUtensorMap* map = maps.m[t.job];
-      const int row_w = t.mb * 256 + cta * 128 + sub * 32, m = row_w + lane, n_tile = t.nb * OUT_COLS;
-      const uint32_t ab = tl & 1, pt = (tl >> 1) & 1;
+      const int row_w = t.mb * C::TILE_ROWS + part * 256 + cta * 128 + sub * 32, m = row_w + lane;
+      const int n_tile = t.nb * OUT_COLS;
+      const uint32_t ab = n & 1, pt = (n >> 1) & 1;
       // the bias of this warp's columns, two a word, words 0-31 and 32-63 over the lanes (gated: g's, u's)
       uint32_t bias_w[2] = {0u, 0u};
       if (!GRAD) {
-        const int n = n_tile + c0 + 2 * lane;
-        if (p.bias && 2 * lane < PER && n < j.N) bias_w[0] = ld_nc32(p.bias + n);
+        const int col = n_tile + c0 + 2 * lane;
+        if (p.bias && 2 * lane < PER && col < j.N) bias_w[0] = ld_nc32(p.bias + col);
         if (GATED) {
-          if (p.bias2 && 2 * lane < PER && n < j.N) bias_w[1] = ld_nc32(p.bias2 + n);
-        } else if (p.bias && 2 * lane + 64 < PER && n + 64 < j.N) {
-          bias_w[1] = ld_nc32(p.bias + n + 64);
+          if (p.bias2 && 2 * lane < PER && col < j.N) bias_w[1] = ld_nc32(p.bias2 + col);
+        } else if (p.bias && 2 * lane + 64 < PER && col + 64 < j.N) {
+          bias_w[1] = ld_nc32(p.bias + col + 64);
         }
       }
       // eight columns c .. c + 7 of the warp's: v += bias (words of reg)
@@ -550,7 +621,8 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
       uint4 res[2] = {residual8(m, n_tile + c0), residual8(m, n_tile + c0 + 8)};
       if (!mbar_wait(smem_u32(&ctl->t_full[ab]), pt, abort_flag, p.err)) break;
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16) + ab * C::ACC_COLS;
+      const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16) + ab * (TALL ? BN : C::ACC_COLS);
+      const bool second = GRAD && t.second;
       auto emit_box = [&](Out out, int at, int c) {
         // the next 16 columns come out of TMEM while these are worked on
         uint32_t r[2][16], q[2][GATED ? 16 : 1];
@@ -597,13 +669,14 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
       for (int c = c0; c < c0 + PER; c += W) {
         if (!GRAD && p.Z) emit_box(OUT_Z, MAP_Z, c);
         if (GATED && p.Z2) emit_box(OUT_Z2, MAP_Z2, c);
-        emit_box(OUT_Y, GRAD && t.second ? MAP_Y2 : MAP_Y, c);
+        emit_box(OUT_Y, second ? MAP_Y2 : MAP_Y, c);
       }
       tc_fence_before();
       __syncwarp();
       // not for a buffer no later tile waits for: nothing is left in flight towards the pair's first CTA
-      if (lane == 0 && tile + 2 * step < num_tiles)
-        mbar_arrive_cluster(dsmem_map(smem_u32(&ctl->t_empty[ab]), rank & ~1u));
+      const bool wanted = tile_at((n + 2) / PARTS).valid;
+      if (lane == 0 && wanted) mbar_arrive_cluster(dsmem_map(smem_u32(&ctl->t_empty[ab]), rank & ~1u));
+      if (part == PARTS - 1) t = tile_at((n + 1) / PARTS);
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -653,10 +726,10 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
   };
 
   if (SWAP && warp >= 2 && S == 1) {
-    uint32_t tl = 0;
-    for (int tile = first; tile < num_tiles; tile += step, ++tl) {
-      const Tile t = tile_at(tile);
-      const uint32_t ab = tl & 1, pt = (tl >> 1) & 1;
+    for (int n = 0;; ++n) {
+      const Tile t = tile_at(n);
+      if (!t.valid) break;
+      const uint32_t ab = n & 1, pt = (n >> 1) & 1;
       // the four warps leave together when the wait runs out: emit_tokens joins them
       const bool ok = mbar_wait(smem_u32(&ctl->t_full[ab]), pt, abort_flag, p.err);
       if (!all_warps_ok(ok)) break;
@@ -686,7 +759,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
     const int log_own = LOG_OUT - (31 - __clz(S)), own = 1 << log_own;    // S is a power of two, own >= 4
     const uint32_t line = (own + 4) * 4;
     const uint32_t inbox = smem_u32(C::INBOX ? park + C::PARK : ring) + row * line;
-    const Tile t = tile_at(first);
+    const Tile t = tile_at(0);
     const Gemm16Job& j = p.job[t.job];
     bool ok = false;
     if (warp >= 2) {
@@ -779,10 +852,10 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED>::THREADS, 1)
 
 namespace {
 
-template <int CG, int BN, bool SWAP, bool GATED, bool GRAD, bool FP16>
+template <int CG, int BN, bool SWAP, bool GATED, bool GRAD, bool TALL, bool FP16>
 cudaError_t launch(const Gemm16Maps<2>& maps, const Gemm16Params& p, int num_sms, cudaStream_t stream) {
-  using C = Cfg<CG, BN, SWAP, GATED>;
-  auto kern = gemm16_kernel<CG, BN, SWAP, GATED, GRAD, FP16>;
+  using C = Cfg<CG, BN, SWAP, GATED, TALL>;
+  auto kern = gemm16_kernel<CG, BN, SWAP, GATED, GRAD, TALL, FP16>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)p.job[0].tiles_m * p.job[0].tiles_n + (long long)p.job[1].tiles_m * p.job[1].tiles_n;
@@ -815,10 +888,10 @@ cudaError_t launch(const Gemm16Maps<2>& maps, const Gemm16Params& p, int num_sms
 // it), at least 9, the row blocks shared out evenly.  Measured, back to back:
 // 4608 x 3072 -> 9216 all 18 blocks 189 us, groups of 9 193, 8 195, 4 199;
 // 8192 x 8192 -> 8192 groups of 8 828, 18 855, 4 857.
-int group_rows(const Gemm16Job& j) {
+int group_rows(const Gemm16Job& j, bool tall) {
   if (j.tiles_m == 0) return 1;
-  const long long block = 2ll * 256 * j.nk * BK;
-  const int most = 40000000 / block > 9 ? (int)(40000000 / block) : 9, groups = (j.tiles_m + most - 1) / most;
+  const long long block = 2ll * (tall ? 512 : 256) * j.nk * BK;
+  const int least = tall ? 5 : 9, most = 40000000 / block > least ? (int)(40000000 / block) : least, groups = (j.tiles_m + most - 1) / most;
   return (j.tiles_m + groups - 1) / groups;
 }
 
@@ -828,10 +901,10 @@ cudaError_t launch_as(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, const G
   if (plan.swap) {
 #define SVDQ_SWAP(G)                                                                        \
   switch (plan.bn) {                                                                        \
-    case 16: return launch<1, 16, true, G, false, FP16>(maps, p, num_sms, stream);          \
-    case 32: return launch<1, 32, true, G, false, FP16>(maps, p, num_sms, stream);          \
-    case 64: return launch<1, 64, true, G, false, FP16>(maps, p, num_sms, stream);          \
-    case 128: return launch<1, 128, true, G, false, FP16>(maps, p, num_sms, stream);        \
+    case 16: return launch<1, 16, true, G, false, false, FP16>(maps, p, num_sms, stream);          \
+    case 32: return launch<1, 32, true, G, false, false, FP16>(maps, p, num_sms, stream);          \
+    case 64: return launch<1, 64, true, G, false, false, FP16>(maps, p, num_sms, stream);          \
+    case 128: return launch<1, 128, true, G, false, false, FP16>(maps, p, num_sms, stream);        \
     default: return cudaErrorInvalidValue;                                                  \
   }
     if (plan.op == GEMM16_NT) SVDQ_SWAP(false)
@@ -839,9 +912,14 @@ cudaError_t launch_as(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, const G
 #undef SVDQ_SWAP
     return cudaErrorInvalidValue;
   }
+  if (plan.tall) {
+    if (plan.op == GEMM16_NT) return launch<2, 256, false, false, false, true, FP16>(maps, p, num_sms, stream);
+    if (plan.op == GEMM16_GRAD) return launch<2, 256, false, false, true, true, FP16>(maps, p, num_sms, stream);
+    return cudaErrorInvalidValue;
+  }
 #define SVDQ_PAIR(G, B)                                                                     \
-  return plan.bn == 256 ? launch<2, 256, false, G, B, FP16>(maps, p, num_sms, stream)       \
-                        : launch<2, 128, false, G, B, FP16>(maps, p, num_sms, stream);
+  return plan.bn == 256 ? launch<2, 256, false, G, B, false, FP16>(maps, p, num_sms, stream) \
+                        : launch<2, 128, false, G, B, false, FP16>(maps, p, num_sms, stream);
   switch (plan.op) {
     case GEMM16_NT: SVDQ_PAIR(false, false)
     case GEMM16_GATED: SVDQ_PAIR(true, false)
@@ -856,8 +934,9 @@ cudaError_t launch_as(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, const G
 cudaError_t launch_gemm16(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, Gemm16Params p, int num_sms,
                           cudaStream_t stream) {
   p.splits = plan.splits;
-  p.job[0].group = group_rows(p.job[0]);
-  p.job[1].group = group_rows(p.job[1]);
+  p.job[0].group = group_rows(p.job[0], plan.tall);
+  p.job[1].group = group_rows(p.job[1], plan.tall);
+  p.job1_extra = gemm16_extra(p.job[0].nk, p.job[1].nk);
   return p.fp16 ? launch_as<true>(plan, maps, p, num_sms, stream) : launch_as<false>(plan, maps, p, num_sms, stream);
 }
 

@@ -250,6 +250,7 @@ struct Gemm16Plan {
   bool swap;     // the weight is the MMA's 128-row operand, the tokens its N
   int bn;        // MMA N: 128 or 256 (pair form), 16, 32, 64 or 128 (swapped)
   int splits;    // CTAs (pairs) a tile's reduction is split over: a power of two
+  bool tall;     // pair form: 512 x 256 tiles (NT and GRAD, not split)
 };
 struct Gemm16Job {
   int M, N;                    // rows and columns of the output (of each of two stacked ones)
@@ -263,7 +264,7 @@ struct Gemm16Job {
 };
 struct Gemm16Params {
   Gemm16Job job[2];            // the second: GRAD only
-  int splits;                  // set by the launcher
+  int splits, job1_extra;      // set by the launcher
   int fp16;                    // 0 bf16, 1 fp16
   // forward epilogue
   int act;                     // svdq_epilogue
@@ -283,6 +284,8 @@ template <int JOBS>
 struct Gemm16Maps {
   CUtensorMap m[JOBS][MAPS];
 };
+// Tiles of the second job that make up for one of the first.
+constexpr int gemm16_extra(int nk0, int nk1) { return nk1 > 0 ? (nk0 + nk1 / 2) / nk1 : 0; }
 // Columns of the pair form's store boxes (32 rows high; 128-byte swizzle, 64-byte for 32 columns).
 constexpr int gemm16_box_cols(const Gemm16Plan& p) { return p.op == GEMM16_GATED && p.bn == 128 ? 32 : 64; }
 cudaError_t launch_gemm16(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, Gemm16Params p, int num_sms,
