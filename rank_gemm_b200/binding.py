@@ -338,6 +338,8 @@ def _rows(t, rows, cols, dt, dev, what):
     rows are contiguous."""
     if t is None:
         return None, 0
+    if t.dtype is dt and t.get_device() == dev and t.shape == (rows, cols) and t.is_contiguous():
+        return t.data_ptr(), cols
     st, sh = t.stride(), t.shape
     if t.dtype is not dt or t.get_device() != dev or len(sh) != 2 or sh[1] != cols or sh[0] < rows or \
             (cols > 1 and st[1] != 1):

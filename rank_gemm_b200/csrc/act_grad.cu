@@ -157,33 +157,18 @@ int act_grad_parts(int M, int N) {
   return parts < 1 ? 1 : parts;
 }
 
-// A launch that may be scheduled under the previous kernel's tail.
-template <typename... P, typename... A>
-static cudaError_t launch_early(void (*kern)(P...), dim3 grid, int block, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream) {
   const dim3 grid((p.N + COLS - 1) / COLS, p.parts);
   switch (p.kind) {
-    case ACT_GRAD_SUM: return launch_early(act_grad_kernel<ACT_GRAD_SUM>, grid, THREADS, stream, p);
-    case ACT_GRAD_DENSE: return launch_early(act_grad_kernel<ACT_GRAD_DENSE>, grid, THREADS, stream, p);
-    default: return launch_early(act_grad_kernel<ACT_GRAD_GATED>, grid, THREADS, stream, p);
+    case ACT_GRAD_SUM: return launch_early(act_grad_kernel<ACT_GRAD_SUM>, grid, THREADS, 0, stream, p);
+    case ACT_GRAD_DENSE: return launch_early(act_grad_kernel<ACT_GRAD_DENSE>, grid, THREADS, 0, stream, p);
+    default: return launch_early(act_grad_kernel<ACT_GRAD_GATED>, grid, THREADS, 0, stream, p);
   }
 }
 
 cudaError_t launch_sum_parts(const float* part, int parts, int N, int dt, void* out, const float* part2, void* out2,
                              cudaStream_t stream) {
-  return launch_early(sum_parts_kernel, dim3((N + 31) / 32, part2 ? 2 : 1), 32 * SUM_LANES, stream, part, part2, parts, N,
+  return launch_early(sum_parts_kernel, dim3((N + 31) / 32, part2 ? 2 : 1), 32 * SUM_LANES, 0, stream, part, part2, parts, N,
                       dt, out, out2);
 }
 

@@ -18,6 +18,23 @@ namespace svdq {
 // kernel's launch).
 cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes);
 
+// Launches a kernel that may be scheduled under the previous kernel's tail
+// (it waits with grid_dependency_wait before its first global access).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, int block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // SVDQ_OK when the current device is supported (compute capability 10.0)
 // and holds the handle `w`; the status any entry point would return otherwise.
 svdq_status handle_device_status(const svdq_weights* w);

@@ -277,8 +277,8 @@ __device__ __forceinline__ void group_sums(float (&s)[N], float (*sh)[N], int tp
 static_assert(MAX_TPR <= 16 * 32, "Reducer adds at most 16 warps");
 
 // ------------------------------------------------------------------ rows ahead
-// A thread's ring of row packs in shared memory (16-byte packs), or nothing
-// (one-element packs, which are loaded when they are needed).
+// A thread's ring of row packs in shared memory (16-byte packs); one-element
+// packs are loaded one round ahead into registers instead.
 template <typename P, int PER, int ROWS>
 struct Ring {
   static constexpr bool ON = sizeof(P) == 16;
@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(TPR < SMALL_BLOCK ? SMALL_BLOCK : TPR, PER <= 
   const P* be = static_cast<const P*>(p.beta) + t;
   const bool affine = p.gamma != nullptr;
   Reducer red(sh, TPR);
-  const Ring<P, PER, 1> ring{smem_u32(ring_raw)};
+  using RowRing = Ring<P, PER, 1>;
+  const RowRing ring{smem_u32(ring_raw)};
   const float inv_c = 1.0f / (float)p.C;
   const long long stride = (long long)gridDim.x * RPB;
   long long row = (long long)blockIdx.x * RPB + g0;
@@ -330,29 +331,45 @@ __global__ void __launch_bounds__(TPR < SMALL_BLOCK ? SMALL_BLOCK : TPR, PER <= 
     cp_commit();
     src += step;
   };
-  if (ring.ON)
+  P ahead[RowRing::ON ? 1 : PER];
+  auto load = [&](long long r) {   // one-element packs of the row at src
+    if (r < p.M)
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i * TPR < left) ahead[i] = reinterpret_cast<const P*>(src)[i * TPR];
+    src += step;
+  };
+  grid_launch_dependents();
+  grid_dependency_wait();
+  if constexpr (RowRing::ON) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) fetch(row + d * stride, d);
+  } else {
+    load(row);
+  }
   int stage = 0;
   // every group of a block runs the same number of rounds (the reductions' barriers)
   for (long long base = (long long)blockIdx.x * RPB; base < p.M; base += stride, row += stride) {
     const bool live = row < p.M;
-    if (ring.ON) cp_wait_oldest();
+    if (RowRing::ON) cp_wait_oldest();
     float x[PER][VEC];
     F2 acc = both(0.f), acc2 = both(0.f);   // two chains: half the latency
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (live && i * TPR < left) {
-        unpack<T, VEC>(ring.ON ? ring.get(stage, 0, i) : reinterpret_cast<const P*>(src)[i * TPR], x[i]);
+        if constexpr (RowRing::ON)
+          unpack<T, VEC>(ring.get(stage, 0, i), x[i]);
+        else
+          unpack<T, VEC>(ahead[i], x[i]);
         add_to<VEC>(i & 1 ? acc2 : acc, x[i]);
       }
     acc = add2(acc, acc2);
     const float mean = red.sum1(acc.x + acc.y) * inv_c;
-    if (ring.ON) {   // the slots have been read: the sum above needed their values
+    if constexpr (RowRing::ON) {   // the slots have been read: the sum above needed their values
       fetch(row + DEPTH * stride, stage);
       stage = stage + 1 == DEPTH ? 0 : stage + 1;
     } else {
-      src += step;
+      load(row + stride);
     }
     acc = acc2 = both(0.f);
 #pragma unroll
@@ -437,11 +454,14 @@ __global__ void __launch_bounds__(MAX_TPR) layernorm_grad_kernel(LayerNormGradPa
   const int rpb = blockDim.x / tpr, t = threadIdx.x % tpr, g0 = threadIdx.x / tpr;
   const int left = p.C / VEC - t;   // pack i is the row's while i tpr < left
   using P = typename PackOf<T, VEC>::type;
-  const Ring<P, PER, 2 * R> ring{smem_u32(ring_raw)};
+  using RowRing = Ring<P, PER, 2 * R>;
+  const RowRing ring{smem_u32(ring_raw)};
   const float inv_c = 1.0f / (float)p.C;
   constexpr bool KEEP = PER * VEC <= 16;   // gamma in registers
   const P* ga = static_cast<const P*>(p.gamma);
   float ag[PER][VEC], ab[PER][VEC], gam[KEEP ? PER : 1][VEC];
+  grid_launch_dependents();
+  grid_dependency_wait();
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
 #pragma unroll
@@ -474,9 +494,26 @@ __global__ void __launch_bounds__(MAX_TPR) layernorm_grad_kernel(LayerNormGradPa
     cp_commit();
     ahead += round;
   };
-  if (ring.ON)
+  P ax[R][RowRing::ON ? 1 : PER], ad[R][RowRing::ON ? 1 : PER];
+  auto load = [&](long long m0) {   // one-element packs of a round
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (m0 + r * stride < p.M) {
+        const P *x = x_of(m0 + r * stride), *d = dy_of(m0 + r * stride);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (i * tpr < left) {
+            ax[r][i] = x[i * tpr];
+            ad[r][i] = d[i * tpr];
+          }
+      }
+  };
+  if constexpr (RowRing::ON) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) fetch(d);
+  } else {
+    load(row);
+  }
   float next_mean[R], next_rstd[R];
   auto fetch_stats = [&](long long m0) {
 #pragma unroll
@@ -497,7 +534,7 @@ __global__ void __launch_bounds__(MAX_TPR) layernorm_grad_kernel(LayerNormGradPa
       rstd[r] = next_rstd[r];
     }
     fetch_stats(row + round);
-    if (ring.ON) cp_wait_oldest();
+    if (RowRing::ON) cp_wait_oldest();
     float xh[R][PER][VEC], g[R][PER][VEC];   // normalized values; dy, then dy gamma
     float s[2 * R];
 #pragma unroll
@@ -507,8 +544,13 @@ __global__ void __launch_bounds__(MAX_TPR) layernorm_grad_kernel(LayerNormGradPa
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         if (live && i * tpr < left) {
-          unpack<T, VEC>(ring.ON ? ring.get(stage, 2 * r, i) : x_of(row + r * stride)[i * tpr], xh[r][i]);
-          unpack<T, VEC>(ring.ON ? ring.get(stage, 2 * r + 1, i) : dy_of(row + r * stride)[i * tpr], g[r][i]);
+          if constexpr (RowRing::ON) {
+            unpack<T, VEC>(ring.get(stage, 2 * r, i), xh[r][i]);
+            unpack<T, VEC>(ring.get(stage, 2 * r + 1, i), g[r][i]);
+          } else {
+            unpack<T, VEC>(ax[r][i], xh[r][i]);
+            unpack<T, VEC>(ad[r][i], g[r][i]);
+          }
           add_s<VEC>(xh[r][i], xh[r][i], -mean[r]);
           mul_s<VEC>(xh[r][i], xh[r][i], rstd[r]);
           fma_v<VEC>(ag[i], g[r][i], xh[r][i], ag[i]);
@@ -527,9 +569,11 @@ __global__ void __launch_bounds__(MAX_TPR) layernorm_grad_kernel(LayerNormGradPa
       s[2 * r + 1] = s1.x + s1.y;
     }
     group_sums<2 * R>(s, sh, tpr, buf);
-    if (ring.ON) {   // the slots have been read: the sums above needed their values
+    if constexpr (RowRing::ON) {   // the slots have been read: the sums above needed their values
       fetch(stage);
       stage = stage + 1 == DEPTH ? 0 : stage + 1;
+    } else {
+      load(row + round);
     }
     if (p.dX) {
 #pragma unroll
@@ -657,8 +701,7 @@ cudaError_t walk(void (*kern)(Params, Args...), const Params& p, int block, int 
   }
   if (grid > most) grid = most;
   *blocks = grid;
-  kern<<<grid, block, smem, st>>>(p, args...);
-  return cudaGetLastError();
+  return launch_early(kern, dim3(grid), block, smem, st, p, args...);
 }
 
 constexpr int FEW_ROWS = 148 * 4;
@@ -719,7 +762,7 @@ template <typename T, int VEC>
 cudaError_t backward(const LayerNormGradParams& p, int* parts, cudaStream_t st) {
   const int nv = p.C / VEC, most = layernorm_grad_parts(p.M, p.C);
   if constexpr (VEC == 1) {
-    if (nv <= 2 * MAX_TPR) return backward_as<T, VEC, 2>(p, most, parts, st);
+    if (nv <= (p.M <= FEW_ROWS ? 2 * MAX_TPR : 64)) return backward_as<T, VEC, 2>(p, most, parts, st);
     if (nv <= 8 * MAX_TPR) return backward_as<T, VEC, 8>(p, most, parts, st);
     if (nv <= 16 * MAX_TPR) return backward_as<T, VEC, 16>(p, most, parts, st);
   } else {
