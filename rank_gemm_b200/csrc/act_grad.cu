@@ -12,7 +12,7 @@
 // of a column write one float32 partial each, and sum_parts_kernel adds those
 // in order: no atomics, the same bits on every run.
 #include "common.cuh"
-#include "kernels.h"
+#include "dense.h"
 
 namespace svdq {
 

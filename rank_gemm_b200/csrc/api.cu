@@ -16,6 +16,7 @@
 
 #include "svdq.h"
 #include "common.cuh"
+#include "dense.h"
 #include "kernels.h"
 
 using namespace svdq;

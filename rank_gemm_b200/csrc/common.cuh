@@ -46,20 +46,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return u;
 }
 
-// Read-only loads of data no kernel writes meanwhile.  Volatile, so that a
-// load guarded by a null check is never issued ahead of the check; without a
-// memory clobber, so that it may still move ahead of earlier stores.
-__device__ __forceinline__ uint4 ld_nc(const uint4* p) {
-  uint4 u;
-  asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
-  return u;
-}
-__device__ __forceinline__ uint16_t ld_nc(const uint16_t* p) {
-  uint16_t u;
-  asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(u) : "l"(p));
-  return u;
-}
-
 // ----------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -419,36 +405,6 @@ __device__ __forceinline__ float gelu_tanh(float y) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(-kTwoULog2e * z));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
   return y * r;
-}
-
-// SiLU, y / (1 + e^-y), with the same two approximations (relative error near
-// 1e-6 for a 16-bit output).
-__device__ __forceinline__ float sigmoid_approx(float y) {
-  float t, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(-1.4426950408889634f * y));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
-  return r;
-}
-__device__ __forceinline__ float silu(float y) { return y * sigmoid_approx(y); }
-
-// (act(z), act'(z)) of an svdq_epilogue.  Both activations are z s(w) with s
-// the logistic function (silu: w = z; tanh-form GELU: w = 2u, u = sqrt(2/pi)
-// (z + 0.044715 z^3)), so act' = s + z s (1 - s) w'.  Where s (1 - s) is 0 the
-// second term is left out: w' may have overflowed there.
-__device__ __forceinline__ void act_and_slope(float z, int act, float& f, float& slope) {
-  if (act == 0) {
-    f = z;
-    slope = 1.f;
-    return;
-  }
-  const bool gelu = act == 1;
-  constexpr float k2 = 1.5957691216057308f;   // 2 sqrt(2/pi)
-  const float zz = z * z;
-  const float w = gelu ? k2 * z * fmaf(0.044715f, zz, 1.0f) : z;
-  const float dw = gelu ? k2 * fmaf(0.134145f, zz, 1.0f) : 1.0f;
-  const float s = sigmoid_approx(w), q = s * (1.0f - s);
-  f = z * s;
-  slope = q > 0.f ? fmaf(z * q, dw, s) : s;
 }
 
 // ----------------------------------------------------------------- 4-bit group quantizers

@@ -10,7 +10,7 @@
 
 #include "svdq.h"
 #include "common.cuh"
-#include "kernels.h"
+#include "dense.h"
 
 using namespace svdq;
 

@@ -46,7 +46,7 @@
 #include <type_traits>
 
 #include "common.cuh"
-#include "kernels.h"
+#include "dense.h"
 
 namespace svdq {
 

@@ -18,43 +18,9 @@ namespace svdq {
 // kernel's launch).
 cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes);
 
-// Launches a kernel that may be scheduled under the previous kernel's tail
-// (it waits with grid_dependency_wait before its first global access).
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*kern)(P...), dim3 grid, int block, size_t smem, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 // SVDQ_OK when the current device is supported (compute capability 10.0)
 // and holds the handle `w`; the status any entry point would return otherwise.
 svdq_status handle_device_status(const svdq_weights* w);
-
-// The current device's SM count and error word, with the status any entry
-// point returns when the device is not supported.
-struct DeviceInfo {
-  int num_sms;
-  DeviceErr err;
-};
-svdq_status current_device_info(DeviceInfo* info);
-
-// 2-D tensor map over row-major [rows][inner], 128-byte swizzled boxes; false
-// when the driver refuses it.
-bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t rows,
-                          uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows,
-                          CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
-
-// A CUDA status as an entry point returns it (clears a non-sticky error).
-svdq_status cuda_status(cudaError_t e);
 
 // ---------------------------------------------------------------- kernel 1
 struct K1Params {
@@ -255,99 +221,5 @@ cudaError_t launch_awq_gemv(const CUtensorMap& tmCode, const CUtensorMap& tmScal
                            AwqParams p, int num_sms, cudaStream_t stream);
 int awq_rows_per_block(int K, int M);
 size_t awq_smem_bytes(int K, int mb);
-
-// ---------------------------------------------------------------- 16-bit matrix products (gemm16.cu)
-// What is multiplied.  NT: both operands with the reduction index innermost
-// (X W^T).  GATED: NT with two weights and the gated epilogue.  GRAD: the
-// backward products, dZ^T X (both operands with the reduction index outermost)
-// and dZ W (B with it outermost), as the jobs of one launch.
-enum Gemm16Op { GEMM16_NT, GEMM16_GATED, GEMM16_GRAD };
-struct Gemm16Plan {
-  Gemm16Op op;
-  bool swap;     // the weight is the MMA's 128-row operand, the tokens its N
-  int bn;        // MMA N: 128 or 256 (pair form), 16, 32, 64 or 128 (swapped)
-  int splits;    // CTAs (pairs) a tile's reduction is split over: a power of two
-  bool tall;     // pair form: 512 x 256 tiles (NT and GRAD, not split)
-};
-struct Gemm16Job {
-  int M, N;                    // rows and columns of the output (of each of two stacked ones)
-  int tiles_m, tiles_n;        // tiles along the MMA's M and N; 0: no such job
-  int tiles_m1;                // row blocks of the first of two stacked A operands (tiles_m: one)
-  int nk1, nk;                 // 64-wide k-tiles of the first operand pair, of both
-  int group;                   // set by the launcher: row blocks of a group of tiles
-  int a_mn;                    // GRAD: A has the reduction index outermost
-  uint16_t *Y, *Y2;            // output rows of stride ldy; the second stacked output
-  long long ldy;
-};
-struct Gemm16Params {
-  Gemm16Job job[2];            // the second: GRAD only
-  int splits, job1_extra;      // set by the launcher
-  int fp16;                    // 0 bf16, 1 fp16
-  // forward epilogue
-  int act;                     // svdq_epilogue
-  const uint16_t *bias, *bias2;
-  const uint16_t* R;           // residual rows of stride ldr, or null
-  long long ldr;
-  uint16_t *Z, *Z2;            // pre-activations [M][N], or null
-  // GRAD: bias gradients from `parts` column-sum partials [parts][part_n] (0: none)
-  int parts, part_n;
-  const float *part, *part2;
-  uint16_t *dbias, *dbias2;
-  DeviceErr err;
-};
-// A job's tensor maps; a map that nothing uses is a copy of another.
-enum Gemm16Map { MAP_A, MAP_A2, MAP_B, MAP_B2, MAP_Y, MAP_Z, MAP_Z2, MAPS, MAP_Y2 = MAP_Z2 };
-template <int JOBS>
-struct Gemm16Maps {
-  CUtensorMap m[JOBS][MAPS];
-};
-// Tiles of the second job that make up for one of the first.
-constexpr int gemm16_extra(int nk0, int nk1) { return nk1 > 0 ? (nk0 + nk1 / 2) / nk1 : 0; }
-// Columns of the pair form's store boxes (32 rows high; 128-byte swizzle, 64-byte for 32 columns).
-constexpr int gemm16_box_cols(const Gemm16Plan& p) { return p.op == GEMM16_GATED && p.bn == 128 ? 32 : 64; }
-cudaError_t launch_gemm16(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, Gemm16Params p, int num_sms,
-                          cudaStream_t stream);
-
-// ---------------------------------------------------------------- column sums and activation slopes (act_grad.cu)
-// Kinds of the pass over [M][N] gradients: column sums alone; dZ = dY act'(Z);
-// dG = dH U act'(G), dU = dH act(G); the last two with optional column sums.
-enum ActGradKind { ACT_GRAD_SUM, ACT_GRAD_DENSE, ACT_GRAD_GATED };
-struct ActGradParams {
-  ActGradKind kind;
-  int M, N, fp16, act;
-  const uint16_t* dY;          // rows of stride ld
-  long long ld;
-  const uint16_t *Z, *U;       // [M][N]
-  uint16_t *dZ, *dU;           // [M][N]
-  float *part, *part2;         // [parts][N] column-sum partials, or null
-  int parts;                   // act_grad_parts(M, N)
-};
-int act_grad_parts(int M, int N);
-cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream);
-// out[n] = round(sum over parts, in order, of part[.][n]), dt svdq_dtype
-cudaError_t launch_sum_parts(const float* part, int parts, int N, int dt, void* out, const float* part2, void* out2,
-                             cudaStream_t stream);
-
-// ---------------------------------------------------------------- layer norm (layernorm.cu)
-struct LayerNormParams {
-  int M, C, dt;                // svdq_dtype
-  const void *X, *gamma, *beta;
-  long long ldx, ldy;
-  float eps;
-  void* Y;
-  float *mean, *rstd;          // [M], or null
-};
-cudaError_t launch_layernorm(const LayerNormParams& p, cudaStream_t stream);
-struct LayerNormGradParams {
-  int M, C, dt;
-  const void *dY, *X, *gamma;
-  long long lddy, ldx, lddx;
-  const float *mean, *rstd;
-  void* dX;
-  float *part_g, *part_b;      // [parts][C] partials of dgamma / dbeta, or null
-};
-int layernorm_grad_parts(int M, int C);   // partials at most
-// *parts: the partials it writes
-cudaError_t launch_layernorm_grad(const LayerNormGradParams& p, int* parts, cudaStream_t stream);
 
 }  // namespace svdq

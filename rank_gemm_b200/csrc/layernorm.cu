@@ -19,7 +19,7 @@
 #include <type_traits>
 
 #include "common.cuh"
-#include "kernels.h"
+#include "dense.h"
 
 namespace svdq {
 
