@@ -138,17 +138,24 @@ int layernorm_grad_parts(int M, int C);   // partials at most
 cudaError_t launch_layernorm_grad(const LayerNormGradParams& p, int* parts, cudaStream_t stream);
 
 // ---------------------------------------------------------------- device helpers
-// Read-only loads of data no kernel writes meanwhile.  Volatile, so that a
-// load guarded by a null check is never issued ahead of the check; without a
-// memory clobber, so that it may still move ahead of earlier stores.
-__device__ __forceinline__ uint4 ld_nc(const uint4* p) {
+// Loads of gamma, beta and biases.  Volatile, so that a load guarded by a null
+// check is never issued ahead of the check; without a memory clobber, so that
+// it may still move ahead of earlier stores.  Not the read-only (.nc) form:
+// these kernels start under the previous one's tail, which may be writing
+// what they read after grid_dependency_wait.
+__device__ __forceinline__ uint4 ld_param(const uint4* p) {
   uint4 u;
-  asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
   return u;
 }
-__device__ __forceinline__ uint16_t ld_nc(const uint16_t* p) {
+__device__ __forceinline__ uint32_t ld_param32(const void* p) {
+  uint32_t u;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(u) : "l"(p));
+  return u;
+}
+__device__ __forceinline__ uint16_t ld_param(const uint16_t* p) {
   uint16_t u;
-  asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(u) : "l"(p));
+  asm volatile("ld.global.b16 %0, [%1];" : "=h"(u) : "l"(p));
   return u;
 }
 

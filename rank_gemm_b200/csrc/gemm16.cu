@@ -203,12 +203,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-__device__ __forceinline__ uint32_t ld_nc32(const void* p) {   // see ld_nc
-  uint32_t u;
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(u) : "l"(p));
-  return u;
-}
-
 // Tile of one operand, k step j (16 wide).  K-major: 128-byte rows, 8-row
 // groups 1024 bytes apart, a step 32 bytes into the row.  MN-major: boxes of
 // 64 (MN) x 64 (k), a k row of 64 MN values per 128-byte line, 8-k groups
@@ -231,14 +225,14 @@ __device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 __device__ __forceinline__ float load16(const uint16_t* p, bool fp16) {
-  return unpack16((uint32_t)ld_nc(p), fp16).x;
+  return unpack16((uint32_t)ld_param(p), fp16).x;
 }
 __device__ __forceinline__ uint16_t round16(float v, bool fp16) { return (uint16_t)pack16(v, 0.f, fp16); }
 
 // Eight consecutive columns of one row: v += bias.
 __device__ __forceinline__ void add_bias8(float (&v)[8], const uint16_t* bias, int n, bool fp16) {
   if (!bias) return;
-  const uint4 b = ld_nc(reinterpret_cast<const uint4*>(bias + n));
+  const uint4 b = ld_param(reinterpret_cast<const uint4*>(bias + n));
   const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -602,11 +596,11 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
       uint32_t bias_w[2] = {0u, 0u};
       if (!GRAD) {
         const int col = n_tile + c0 + 2 * lane;
-        if (p.bias && 2 * lane < PER && col < j.N) bias_w[0] = ld_nc32(p.bias + col);
+        if (p.bias && 2 * lane < PER && col < j.N) bias_w[0] = ld_param32(p.bias + col);
         if (GATED) {
-          if (p.bias2 && 2 * lane < PER && col < j.N) bias_w[1] = ld_nc32(p.bias2 + col);
+          if (p.bias2 && 2 * lane < PER && col < j.N) bias_w[1] = ld_param32(p.bias2 + col);
         } else if (p.bias && 2 * lane + 64 < PER && col + 64 < j.N) {
-          bias_w[1] = ld_nc32(p.bias + col + 64);
+          bias_w[1] = ld_param32(p.bias + col + 64);
         }
       }
       // eight columns c .. c + 7 of the warp's: v += bias (words of reg)

@@ -75,11 +75,11 @@ __device__ __forceinline__ void unpack(const typename PackOf<T, VEC>::type& p, f
     }
   }
 }
-// A pack of gamma or beta (guarded by a null check: see ld_nc).
+// A pack of gamma or beta (guarded by a null check: see ld_param).
 template <typename T, int VEC>
 __device__ __forceinline__ typename PackOf<T, VEC>::type ld_const(const typename PackOf<T, VEC>::type* p) {
   if constexpr (VEC > 1)
-    return ld_nc(p);
+    return ld_param(p);
   else
     return *p;
 }

@@ -342,6 +342,36 @@ def test_special_values_stay_in_their_row_and_column(B, M):
     assert bool((Y[11, cols] <= -3e38).all())
 
 
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_columns_between_rows_are_not_read(B, M):
+    """NaN in the columns between a row's end and the next row's start."""
+    t, K, N = torch.float16, 72, 136
+    g = D.gen(13)
+    X, dY, R = D.nan_like(t, M, K + 56), D.nan_like(t, M, N + 56), D.nan_like(t, M, N + 56)
+    X[:, :K], dY[:, :N], R[:, :N] = D.draw(g, t, M, K), D.draw(g, t, M, N), D.draw(g, t, M, N)
+    W, Z = D.draw(g, t, N, K, scale=0.05), D.draw(g, t, M, N)
+    Y, H, dX, dX2, n = (D.nan_like(t, M, w) for w in (N, N, K, K, K))
+    dW, dW2, dW3, db = D.nan_like(t, N, K), D.nan_like(t, N, K), D.nan_like(t, N, K), D.nan_like(t, N)
+    x, dy = X[:, :K], dY[:, :N]
+    ws = torch.empty(B.svdq_gated_linear_backward_workspace_bytes(M, K, N), dtype=torch.uint8, device="cuda")
+    B.svdq_dense_linear(M, K, N, x, W, None, 0, R[:, :N], Y)
+    B.svdq_gated_linear(M, K, N, x, W, W, None, None, 1, H)
+    B.svdq_dense_linear_backward(M, K, N, dy, x, W, None, 0, dX, dW, db, ws)
+    B.svdq_gated_linear_backward(M, K, N, dy, x, W, W, Z, Z, 1, dX2, dW2, dW3, None, None, ws)
+    B.svdq_layernorm(M, K, x, None, None, 1e-5, n)
+    for out in (Y, H, dX, dW, db, dX2, dW2, dW3, n):
+        assert bool(out.isfinite().all())
+
+
+@pytest.mark.parametrize("t,M,C,ld", [(BF, 700, 512, 512), (torch.float32, 40, 1001, 1003), (torch.float16, 3, 40000, 40000)])
+def test_layernorm_in_place(B, t, M, C, ld):
+    X = D.draw(D.gen(14), t, M, ld)[:, :C]
+    Y = D.nan_like(t, M, C)
+    B.svdq_layernorm(M, C, X, None, None, 1e-5, Y)
+    B.svdq_layernorm(M, C, X, None, None, 1e-5, X)
+    assert torch.equal(X, Y)
+
+
 def test_zero_and_constant_rows(B):
     """A constant row: variance 0, rstd = 1 / sqrt(eps), the output is beta; with eps = 0 a NaN, as 0 * inf."""
     t, M, C = torch.float32, 4, 100
