@@ -9,8 +9,12 @@
 //   each output rounded once from float32.
 //
 // One kernel template, warp-specialised: warp 0 feeds a ring of k-tiles
-// (64 wide) by TMA, warp 1 issues the MMAs from one thread, the other warps
-// drain the accumulators.
+// (64 wide) by TMA, warp 1 issues the MMAs, the other warps drain the
+// accumulators.  The MMA warp runs its loop whole and elects a lane for each
+// issue: state that is uniform over the warp reaches the instructions' uniform
+// operands without a move, and that warp's instructions between two MMAs bound
+// the shorter tiles (256 rows 3072 -> 9216: 17.5 us with a single-lane loop,
+// 15.6 so).
 //   pair form (CG = 2)    a CTA pair shares one 256 x BN tile
 //                         (tcgen05.mma.cta_group::2): each CTA stages its 128
 //                         rows of A and its half of B, so an operand byte is
@@ -72,7 +76,7 @@ struct Cfg {
   static constexpr int A_BYTES = A_TILES * A_TILE_BYTES;
   static constexpr int B_ROWS = BN / CG;                  // per CTA
   static constexpr int B_BYTES = B_ROWS * BK * 2;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int K_TILE = A_BYTES + B_BYTES;          // one 64-wide k-tile
   static constexpr int OUT_COLS = (GATED && !SWAP) ? BN / 2 : BN;   // output columns of a tile
   static constexpr int BOX_COLS = OUT_COLS / 2 < 64 ? OUT_COLS / 2 : 64;   // pair form: columns of a store box
   static constexpr int EPI_WARPS = SWAP ? 4 : 8;          // one or two per TMEM sub-partition
@@ -83,8 +87,13 @@ struct Cfg {
   // rank's MMAs then), else the ring.
   static constexpr int INBOX_WANT = (ACC_COLS + 32 * A_TILES) * 512;
   static constexpr int INBOX =
-      SWAP && (SMEM_LIMIT - 1024 - PARK - INBOX_WANT - (int)sizeof(Ctl)) / STAGE >= 5 ? INBOX_WANT : 0;
-  static constexpr int ROOM = (SMEM_LIMIT - 1024 - PARK - INBOX - (int)sizeof(Ctl)) / STAGE;
+      SWAP && (SMEM_LIMIT - 1024 - PARK - INBOX_WANT - (int)sizeof(Ctl)) / K_TILE >= 5 ? INBOX_WANT : 0;
+  static constexpr int ROOM_BYTES = SMEM_LIMIT - 1024 - PARK - INBOX - (int)sizeof(Ctl);
+  // A stage of the ring is one or two k-tiles: two halve the waits and commits
+  // between the MMAs, where at least four such stages fit.
+  static constexpr int KS = ROOM_BYTES / (2 * K_TILE) >= 4 ? 2 : 1;
+  static constexpr int STAGE = KS * K_TILE;
+  static constexpr int ROOM = ROOM_BYTES / STAGE;
   static constexpr int STAGES = ROOM < MAX_STAGES ? ROOM : MAX_STAGES;
   static constexpr int TMEM_COLS = TALL ? ACC_COLS : pow2_at_least(2 * ACC_COLS, 32);
   static constexpr int THREADS = 32 * (2 + EPI_WARPS);
@@ -95,6 +104,12 @@ struct Cfg {
 };
 
 // ------------------------------------------------------------------ PTX forms this kernel adds
+// True in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -371,6 +386,12 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      auto next = [&] {
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      };
       for (int n = 0; ok; ++n) {
         const Tile t = tile_at(n);
         if (!t.valid) break;
@@ -380,68 +401,60 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
         const int a_row = t.mb * C::TILE_ROWS + cta * 128;
         const int b_row = (GATED && !SWAP) ? t.nb * OUT_COLS : t.nb * BN + cta * C::B_ROWS;
         const int kt1 = k_end(j);
-        for (int kt = k_begin(j); kt < kt1; ++kt) {
-          if (!mbar_wait(smem_u32(&ctl->empty[stage]), phase ^ 1, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
-          const bool seg = GRAD && kt >= j.nk1;               // the second part of a two-part reduction
-          const int k = (seg ? kt - j.nk1 : kt) * BK;
-          const uint32_t a = smem_u32(ring + stage * C::STAGE), b = a + C::A_BYTES;
+        for (int k0 = k_begin(j); k0 < kt1; k0 += C::KS, next()) {
+          if (!(ok = mbar_wait(smem_u32(&ctl->empty[stage]), phase ^ 1, abort_flag, p.err))) break;
           const uint32_t bar = smem_u32(&ctl->full[stage]);
           const uint32_t sig = CG == 2 ? dsmem_map(bar, rank & ~1u) : bar;
-          if (cta == 0) mbar_arrive_expect_tx(bar, CG * C::STAGE);
-          auto load = [&](uint32_t dst, const CUtensorMap* m, int x, int y) {
-            if (CG == 2)
-              tma_load_2d_pair(dst, m, x, y, sig);
-            else
-              tma_load_2d(dst, m, x, y, sig);
-          };
-          auto load_tile = [&](uint32_t dst, const CUtensorMap* m, bool mn, int rows, int row) {
-            if (!mn) {
-              load(dst, m, k, row);
-            } else {
-              for (int i = 0; i < rows; i += 64) load(dst + i * 128, m, row + i, k);
-            }
-          };
-          const CUtensorMap* map_a = map + (t.second || seg ? MAP_A2 : MAP_A);
-          load_tile(a, map_a, a_mn, 128, a_row);
-          if (TALL) load_tile(a + C::A_TILE_BYTES, map_a, a_mn, 128, a_row + 256);
-          if (SWAP && GATED) load_tile(a + C::A_TILE_BYTES, map + MAP_A2, false, 128, a_row);
-          const bool b2 = (GATED && !SWAP) ? cta == 1 : seg;
-          load_tile(b, map + (b2 ? MAP_B2 : MAP_B), GRAD, C::B_ROWS, b_row);
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1;
+          if (cta == 0) mbar_arrive_expect_tx(bar, CG * C::K_TILE * min(C::KS, kt1 - k0));
+          for (int s = 0; s < C::KS && k0 + s < kt1; ++s) {
+            const bool seg = GRAD && k0 + s >= j.nk1;           // the second part of a two-part reduction
+            const int k = (seg ? k0 + s - j.nk1 : k0 + s) * BK;
+            const uint32_t a = smem_u32(ring + stage * C::STAGE + s * C::K_TILE), b = a + C::A_BYTES;
+            auto load = [&](uint32_t dst, const CUtensorMap* m, int x, int y) {
+              if (CG == 2)
+                tma_load_2d_pair(dst, m, x, y, sig);
+              else
+                tma_load_2d(dst, m, x, y, sig);
+            };
+            auto load_tile = [&](uint32_t dst, const CUtensorMap* m, bool mn, int rows, int row) {
+              if (!mn) {
+                load(dst, m, k, row);
+              } else {
+                for (int i = 0; i < rows; i += 64) load(dst + i * 128, m, row + i, k);
+              }
+            };
+            const CUtensorMap* map_a = map + (t.second || seg ? MAP_A2 : MAP_A);
+            load_tile(a, map_a, a_mn, 128, a_row);
+            if (TALL) load_tile(a + C::A_TILE_BYTES, map_a, a_mn, 128, a_row + 256);
+            if (SWAP && GATED) load_tile(a + C::A_TILE_BYTES, map + MAP_A2, false, 128, a_row);
+            const bool b2 = (GATED && !SWAP) ? cta == 1 : seg;
+            load_tile(b, map + (b2 ? MAP_B2 : MAP_B), GRAD, C::B_ROWS, b_row);
           }
         }
       }
       // the pair's commits have all arrived before this CTA may leave
-      for (int i = 0; CG == 2 && ok && i < C::STAGES; ++i) {
+      for (int i = 0; CG == 2 && ok && i < C::STAGES; ++i, next())
         ok = mbar_wait(smem_u32(&ctl->empty[stage]), phase ^ 1, abort_flag, p.err);
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (the pair's first CTA)
-    if (lane == 0 && cta == 0) {
+    if (cta == 0) {
       const uint32_t idesc0 = (1u << 4) | (FP16 ? 0u : (1u << 7) | (1u << 10)) | (GRAD ? 1u << 16 : 0u) |
                               ((uint32_t)(BN >> 3) << 17) | ((uint32_t)((128 * CG) >> 4) << 24);
       const uint16_t mask = (uint16_t)(3u << (rank & ~1u));
-      auto commit = [&](uint64_t* bar) {
+      auto commit = [&](uint64_t* bar) {   // by the elected lane
         if (CG == 2)
           tc_commit_pair(smem_u32(bar), mask);
         else
           tc_commit(smem_u32(bar));
       };
-      // a place in the ring
-      struct Slot {
+      // Every lane runs every iteration, also after a wait has run out (`ok`
+      // then skips the waits and the issues): elect.sync needs them all.
+      bool ok = true;
+      struct Slot {   // a place in the ring
         int stage;
         uint32_t phase;
-        __device__ void next() {
+        __device__ __forceinline__ void next() {
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1;
@@ -449,72 +462,78 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
         }
       };
       Slot at{0, 0};
-      auto filled = [&](const Slot& x) {
-        const bool ok = mbar_wait(smem_u32(&ctl->full[x.stage]), x.phase, abort_flag, p.err);
-        tc_fence_after();
-        return ok;
-      };
-      uint32_t idesc = idesc0;
-      bool a_mn = false;
-      // one k-tile into the accumulators [t0, t1) of the tile at column acc
-      auto multiply = [&](const Slot& x, uint32_t acc, int t0, int t1, bool first_k) {
-        const uint32_t a = smem_u32(ring + x.stage * C::STAGE), b = a + C::A_BYTES;
-#pragma unroll
-        for (int k = 0; k < BK / 16; ++k) {
-          const uint64_t db = operand_desc(GRAD, b, k);
-#pragma unroll
-          for (int t = 0; t < C::A_TILES; ++t)
-            if (t >= t0 && t < t1)
-              mma_f16<CG>(acc + t * BN, operand_desc(a_mn, a + t * C::A_TILE_BYTES, k), db, idesc, !first_k || k != 0);
-        }
-      };
       auto drained = [&](int buf, uint32_t use) {
-        const bool ok = mbar_wait(smem_u32(&ctl->t_empty[buf]), (use & 1) ^ 1, abort_flag, p.err);
+        if (ok) ok = mbar_wait(smem_u32(&ctl->t_empty[buf]), (use & 1) ^ 1, abort_flag, p.err);
         tc_fence_after();
-        return ok;
       };
-      bool ok = true;
-      for (uint32_t n = 0; ok; ++n) {
+      for (uint32_t n = 0;; ++n) {
         const Tile tile = tile_at((int)n);
         if (!tile.valid) break;
         const Gemm16Job& job = p.job[tile.job];
-        a_mn = GRAD && job.a_mn;
-        idesc = idesc0 | (a_mn ? 1u << 15 : 0u);
+        const bool a_mn = GRAD && job.a_mn;
+        const uint32_t idesc = idesc0 | (a_mn ? 1u << 15 : 0u);
         const int nk = k_end(job) - k_begin(job);
-        if (!TALL) {
-          const uint32_t ab = n & 1;
-          ok = drained(ab, n >> 1);
-          for (int k = 0; ok && k < nk; ++k, at.next()) {
-            if (!(ok = filled(at))) break;
-            multiply(at, tmem + ab * C::ACC_COLS, 0, C::A_TILES, k == 0);
-            commit(&ctl->empty[at.stage]);
-          }
-          if (ok) commit(&ctl->t_full[ab]);
-        } else {
-          // k-tiles [k0, k1), at most a ring of them: accumulator 0, then 1 and their release
-          auto apart = [&](int k0, int k1, bool last) {
-            Slot x = at;
-            for (int k = k0; k < k1; ++k, x.next()) {
-              if (!filled(x)) return false;
-              multiply(x, tmem, 0, 1, k == 0);
+        // the k-tiles of the stage at x, `left` of the tile's, into accumulators [T0, T1) at column acc
+        auto multiply = [&](const Slot& x, uint32_t acc, auto t0, auto t1, int left, bool first_k) {
+          constexpr int T0 = decltype(t0)::value, T1 = decltype(t1)::value;
+#pragma unroll
+          for (int s = 0; s < C::KS; ++s) {
+            if (s > 0 && s >= left) break;
+            const uint32_t a = smem_u32(ring + x.stage * C::STAGE + s * C::K_TILE), b = a + C::A_BYTES;
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k) {
+              const uint64_t db = operand_desc(GRAD, b, k);
+#pragma unroll
+              for (int t = T0; t < T1; ++t)
+                mma_f16<CG>(acc + t * BN, operand_desc(a_mn, a + t * C::A_TILE_BYTES, k), db, idesc,
+                            !first_k || s != 0 || k != 0);
             }
-            if (last) commit(&ctl->t_full[0]);
-            if (k0 == 0 && !drained(1, n)) return false;
-            for (int k = k0; k < k1; ++k, at.next()) {
-              multiply(at, tmem, 1, 2, k == 0);
+          }
+        };
+        const std::integral_constant<int, 0> T_0;
+        const std::integral_constant<int, 1> T_1;
+        const std::integral_constant<int, C::A_TILES> T_ALL;
+        // stages from k-tile k0 to k1, one after the other
+        auto through = [&](int k0, int k1, uint32_t acc) {
+          for (int k = k0; k < k1; k += C::KS) {
+            if (ok) ok = mbar_wait(smem_u32(&ctl->full[at.stage]), at.phase, abort_flag, p.err);
+            tc_fence_after();
+            if (elect_one() && ok) {
+              multiply(at, acc, T_0, T_ALL, k1 - k, k == 0);
               commit(&ctl->empty[at.stage]);
             }
-            if (last) commit(&ctl->t_full[1]);
-            return true;
-          };
-          const int head = min(nk, C::STAGES), tail = min(nk - head, C::STAGES);
-          ok = drained(0, n) && apart(0, head, nk == head);
-          for (int k = head; ok && k < nk - tail; ++k, at.next()) {
-            if (!(ok = filled(at))) break;
-            multiply(at, tmem, 0, 2, false);
-            commit(&ctl->empty[at.stage]);
+            at.next();
           }
-          if (ok && tail) ok = apart(nk - tail, nk, true);
+        };
+        if (!TALL) {
+          const uint32_t ab = n & 1;
+          drained(ab, n >> 1);
+          through(0, nk, tmem + ab * C::ACC_COLS);
+          if (elect_one() && ok) commit(&ctl->t_full[ab]);
+        } else {
+          // the same k-tiles, at most a ring of them, for accumulator 0 and then for 1, with their release
+          auto apart = [&](int k0, int k1, bool last) {
+            Slot x = at;
+            for (int k = k0; k < k1; k += C::KS, x.next()) {
+              if (ok) ok = mbar_wait(smem_u32(&ctl->full[x.stage]), x.phase, abort_flag, p.err);
+              tc_fence_after();
+              if (elect_one() && ok) multiply(x, tmem, T_0, T_1, k1 - k, k == 0);
+            }
+            if (last && elect_one() && ok) commit(&ctl->t_full[0]);
+            if (k0 == 0) drained(1, n);
+            for (int k = k0; k < k1; k += C::KS, at.next())
+              if (elect_one() && ok) {
+                multiply(at, tmem, T_1, T_ALL, k1 - k, k == 0);
+                commit(&ctl->empty[at.stage]);
+              }
+            if (last && elect_one() && ok) commit(&ctl->t_full[1]);
+          };
+          constexpr int RING = C::STAGES * C::KS;
+          const int head = min(nk, RING), rest = nk - head, tail = min(rest, RING), mid = (rest - tail + C::KS - 1) / C::KS * C::KS;
+          drained(0, n);
+          apart(0, head, nk == head);
+          through(head, head + mid, tmem);
+          if (rest > mid) apart(head + mid, nk, true);
         }
       }
     }
