@@ -37,16 +37,15 @@ int clusters(int width, int num_sms) {
   return width == 1 ? num_sms : width == 2 ? num_sms / 2 : width == 4 ? num_sms * 33 / 148 : num_sms * 15 / 148;
 }
 
-// Estimated time of a plan in SM cycles: rounds of tiles times k-tiles times
-// the cycles of one k-tile, and fixed parts: launch, fill and drain, the
-// exchange of a split tile's partials, the swapped form's epilogue.  The
-// constants fit the times of 17 shapes (1 .. 777 rows, 1024 x 1024 to
-// 12288 x 3072) under every tiling, each within a sixth; a k-tile costs what
-// its operand bytes take into shared memory (40 to 57 bytes a cycle), not its
-// MMAs.  Where the two forms cross (us, best tilings): 64 x 1024 -> 1024
-// swapped 6.1, pair 8.1; 128 x 12288 -> 3072 swapped 25.5, pair 30.2;
-// 256 x 1024 -> 1024 swapped 8.6, pair 8.6; 256 x 3072 -> 9216 swapped 20.3,
-// pair 18.5.
+// Estimated time of a plan in SM cycles: the longest share of a CTA (pair),
+// k-tile by k-tile, or, where that is longer, the time the operand bytes take
+// from L2 (8500 a cycle over the chip) or the weights from memory (3400);
+// besides, a fixed part (launch, fill, epilogue, drain) and the exchange of a
+// split tile's partials.  The constants fit 24 shapes (1 .. 2048 rows, 1024 x
+// 1024 .. 12288 x 3072, one and two weights) under every tiling.  Where the
+// two forms cross (us, best tilings of each): 64 x 1024 -> 1024 swapped 4.9,
+// pair 6.4; 128 x 12288 -> 3072 swapped 24.4, pair 26.7; 128 x 3072 -> 9216
+// swapped 15.8, pair 15.6; 256 x 1024 -> 1024 swapped 8.6, pair 6.6.
 struct Choice {
   Gemm16Plan plan{};
   double cycles = 0;
@@ -78,14 +77,19 @@ long long longest_share(long long ta, long long ca, long long tb, long long cb, 
 Choice plan_pair(Gemm16Op op, JobShape a, JobShape b, int num_sms) {
   Choice best;
   struct Form {
-    int rows, bn, k_tile, tile, exchange;
+    int rows, bn, k_tile, tile, fixed, exchange;
     bool tall;
   };
-  // Cycles of a k-tile, of a tile besides, of a split's exchange.  512 x 256
-  // tiles take 0.94 of the time of two 256 x 256 at 128 k-tiles (8192^3: 826
-  // us, 875), 0.96 at 72 and 1.01 at 48, and leave more pairs idle at the end.
-  const Form forms[3] = {{512, 256, 1130, 6000, 0, true}, {256, 256, 620, 0, 12000, false},
-                         {256, 128, 480, 0, 5000, false}};
+  // Cycles of a k-tile, of a tile besides, of a launch, of a split's exchange
+  // a rank.  512 x 256 tiles take 0.94 of the time of two 256 x 256 at 128
+  // k-tiles (8192^3: 826 us, 875), 0.96 at 72 and 1.01 at 48, and leave more
+  // pairs idle at the end.
+  // The backward products' 64 x 64 boxes cost the narrow form most (1023 rows,
+  // 1160 and 2056 wide: 128 columns 26.3 us, 256 24.0).
+  const bool grad = op == GEMM16_GRAD;
+  const Form forms[3] = {{512, 256, 1020, 6000, 10400, 0, true},
+                         {256, 256, grad ? 560 : 537, 0, 10400, 5000, false},
+                         {256, 128, grad ? 480 : 365, 0, 6700, 3500, false}};
   for (const Form& f : forms) {
     if (f.tall && op == GEMM16_GATED) continue;
     const int out_cols = op == GEMM16_GATED ? f.bn / 2 : f.bn;
@@ -93,13 +97,14 @@ Choice plan_pair(Gemm16Op op, JobShape a, JobShape b, int num_sms) {
       return j.nk ? (long long)j.stacked * ceil_div(j.M, f.rows) * ceil_div(j.N, out_cols) : 0;
     };
     const long long ta = tiles_of(a), tb = tiles_of(b), tiles = ta + tb;
+    const double arrival = ((double)ta * a.nk + (double)tb * b.nk) * (f.rows + f.bn) * 128 / 8500;
     for (int s = 1; s <= (f.tall ? 1 : 4); s *= 2) {
       const int slots = clusters(2 * s, num_sms);
       if (s > 1 && ((ta && a.nk < 4 * s) || (tb && b.nk < 4 * s) || tiles > slots)) break;
-      const long long share = longest_share(ta, (long long)ceil_div(a.nk, s) * f.k_tile + f.tile, tb,
-                                            (long long)ceil_div(b.nk, s) * f.k_tile + f.tile,
-                                            gemm16_extra(a.nk, b.nk), slots);
-      best.offer({op, false, f.bn, s, f.tall}, 9500 + (double)share + (s > 1 ? f.exchange : 0));
+      const double share = (double)longest_share(ta, (long long)ceil_div(a.nk, s) * f.k_tile + f.tile, tb,
+                                                 (long long)ceil_div(b.nk, s) * f.k_tile + f.tile,
+                                                 gemm16_extra(a.nk, b.nk), slots);
+      best.offer({op, false, f.bn, s, f.tall}, f.fixed + std::max(share, arrival) + (s > 1 ? f.exchange * s : 0));
     }
   }
   return best;
@@ -107,16 +112,16 @@ Choice plan_pair(Gemm16Op op, JobShape a, JobShape b, int num_sms) {
 Choice plan_swap(Gemm16Op op, int tokens, int features, int nk, int num_sms) {
   Choice best;
   const int weights = op == GEMM16_GATED ? 2 : 1;
-  const double stream = (double)weights * features * nk * 128 / 3400;   // the weights at HBM's rate
   for (int bn = 16; bn <= 128; bn *= 2) {
     const int tiles = ceil_div(features, 128) * ceil_div(tokens, bn);
-    const double per_k = 400 * weights + 1.3 * bn;
+    const double per_k = (300 + 1.1 * bn) * (weights == 2 ? 1.5 : 1.0);
     for (int s = 1; s <= 8 && 4 * s <= bn; s *= 2) {   // at least four tokens a rank
       const int slots = clusters(s, num_sms);
       if (s > 1 && (nk < 2 * s || tiles > slots)) break;
-      double t = (double)((tiles + slots - 1) / slots) * ceil_div(nk, s) * per_k;
-      if (t < stream) t = stream;
-      best.offer({op, true, bn, s, false}, 8500 + t + 15 * bn + (s > 1 ? 1500 + 45 * bn : 0));
+      const double share = (double)((tiles + slots - 1) / slots) * ceil_div(nk, s) * per_k;
+      // the weights' bytes at memory's rate, or at 41 a cycle and CTA
+      const double stream = (double)weights * features * nk * 128 / std::min(3400.0, 41.0 * tiles * s);
+      best.offer({op, true, bn, s, false}, 5000 + 50 * bn + std::max(share, stream) + (s > 1 ? 1000 + 70 * bn : 0));
     }
     if (bn >= tokens) break;
   }

@@ -83,15 +83,15 @@ struct Cfg {
   static constexpr int PARK = SWAP ? BN * 256 : EPI_WARPS * 32 * BOX_COLS * 2;   // the store box, or one a warp
   static constexpr int ACC_COLS = A_TILES * BN;
   // The partials a split tile's ranks send this one: memory of their own where
-  // five stages still fit beside it (the senders need not wait for this
+  // eight k-tiles still fit beside it (the senders need not wait for this
   // rank's MMAs then), else the ring.
   static constexpr int INBOX_WANT = (ACC_COLS + 32 * A_TILES) * 512;
   static constexpr int INBOX =
-      SWAP && (SMEM_LIMIT - 1024 - PARK - INBOX_WANT - (int)sizeof(Ctl)) / K_TILE >= 5 ? INBOX_WANT : 0;
+      SWAP && (SMEM_LIMIT - 1024 - PARK - INBOX_WANT - (int)sizeof(Ctl)) / K_TILE >= 8 ? INBOX_WANT : 0;
   static constexpr int ROOM_BYTES = SMEM_LIMIT - 1024 - PARK - INBOX - (int)sizeof(Ctl);
   // A stage of the ring is one or two k-tiles: two halve the waits and commits
-  // between the MMAs, where at least four such stages fit.
-  static constexpr int KS = ROOM_BYTES / (2 * K_TILE) >= 4 ? 2 : 1;
+  // between the MMAs, where at least four such stages fit (swapped: three).
+  static constexpr int KS = ROOM_BYTES / (2 * K_TILE) >= (SWAP ? 3 : 4) ? 2 : 1;
   static constexpr int STAGE = KS * K_TILE;
   static constexpr int ROOM = ROOM_BYTES / STAGE;
   static constexpr int STAGES = ROOM < MAX_STAGES ? ROOM : MAX_STAGES;
