@@ -84,12 +84,12 @@ Choice plan_pair(Gemm16Op op, JobShape a, JobShape b, int num_sms) {
   // a rank.  512 x 256 tiles take 0.94 of the time of two 256 x 256 at 128
   // k-tiles (8192^3: 826 us, 875), 0.96 at 72 and 1.01 at 48, and leave more
   // pairs idle at the end.
-  // The backward products' 64 x 64 boxes cost the narrow form most (1023 rows,
-  // 1160 and 2056 wide: 128 columns 26.3 us, 256 24.0).
+  // The backward products' 64 x 64 boxes cost the narrow forms more (1023
+  // rows, 1160 and 2056 wide: 128 columns 26.3 us, 256 24.0).
   const bool grad = op == GEMM16_GRAD;
-  const Form forms[3] = {{512, 256, 1020, 6000, 10400, 0, true},
-                         {256, 256, grad ? 560 : 537, 0, 10400, 5000, false},
-                         {256, 128, grad ? 480 : 365, 0, 6700, 3500, false}};
+  const Form forms[3] = {{512, 256, grad ? 1060 : 1020, 6000, 10400, 0, true},
+                         {256, 256, grad ? 660 : 537, 0, 10400, 5000, false},
+                         {256, 128, grad ? 620 : 365, 0, 6700, 3500, false}};
   for (const Form& f : forms) {
     if (f.tall && op == GEMM16_GATED) continue;
     const int out_cols = op == GEMM16_GATED ? f.bn / 2 : f.bn;
