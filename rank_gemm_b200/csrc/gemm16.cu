@@ -344,11 +344,13 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   // The next kernel may be scheduled as SMs fall idle; this one touches
-  // global memory only after the previous kernel's writes are visible.
+  // global memory only after the previous kernel's writes are visible.  Every
+  // warp waits here: a bounded wait must not count the previous kernel's time.
   grid_launch_dependents();
-  if (warp != 1) grid_dependency_wait();
+  grid_dependency_wait();
 
-  const int first = (int)blockIdx.x / (CG * S), slots = (int)gridDim.x / (CG * S);   // this pair (CTA, cluster), of how many
+  // this pair (CTA, cluster), of how many
+  const int first = (int)blockIdx.x / (CG * S), slots = (int)gridDim.x / (CG * S);
   const int tiles0 = p.job[0].tiles_m * p.job[0].tiles_n, tiles1 = GRAD ? p.job[1].tiles_m * p.job[1].tiles_n : 0;
   // The n-th tile of this pair: its job and block coordinates.  Job 0's tiles
   // go round the pairs; the pairs left with one fewer of them take
@@ -536,7 +538,8 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
             if (last && elect_one() && ok) commit(&ctl->t_full[1]);
           };
           constexpr int RING = C::STAGES * C::KS;
-          const int head = min(nk, RING), rest = nk - head, tail = min(rest, RING), mid = (rest - tail + C::KS - 1) / C::KS * C::KS;
+          const int head = min(nk, RING), rest = nk - head, tail = min(rest, RING);
+          const int mid = (rest - tail + C::KS - 1) / C::KS * C::KS;
           drained(0, n);
           apart(0, head, nk == head);
           through(head, head + mid, tmem);
@@ -771,7 +774,8 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
   if (S > 1) {
     // One tile per cluster.  Rank q sums output columns q own .. of all ranks:
     // each rank sends its float32 partial of them, four columns a store, into
-    // rank q's ring (free once every rank's MMAs are complete) as [source rank]
+    // rank q's inbox (or, where shared memory holds none beside the ring, into
+    // its ring, free once every rank's MMAs are complete) as [source rank]
     // [128 rows][own + 4 columns] (the pad keeps 16-byte accesses of eight
     // rows on different banks), where q adds the sources in rank order.
     constexpr int HALVES = GATED ? 2 : 1, HALF = C::ACC_COLS / HALVES;   // accumulator halves g and u
@@ -878,7 +882,8 @@ cudaError_t launch(const Gemm16Maps<2>& maps, const Gemm16Params& p, int num_sms
   auto kern = gemm16_kernel<CG, BN, SWAP, GATED, GRAD, TALL, FP16>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
-  const long long tiles = (long long)p.job[0].tiles_m * p.job[0].tiles_n + (long long)p.job[1].tiles_m * p.job[1].tiles_n;
+  const long long tiles =
+      (long long)p.job[0].tiles_m * p.job[0].tiles_n + (long long)p.job[1].tiles_m * p.job[1].tiles_n;
   const int width = CG * p.splits;
   const long long most = p.splits > 1 ? tiles : num_sms / CG;   // a split cluster owns one tile
   cudaLaunchConfig_t cfg = {};
@@ -911,7 +916,8 @@ cudaError_t launch(const Gemm16Maps<2>& maps, const Gemm16Params& p, int num_sms
 int group_rows(const Gemm16Job& j, bool tall) {
   if (j.tiles_m == 0) return 1;
   const long long block = 2ll * (tall ? 512 : 256) * j.nk * BK;
-  const int least = tall ? 5 : 9, most = 40000000 / block > least ? (int)(40000000 / block) : least, groups = (j.tiles_m + most - 1) / most;
+  const int least = tall ? 5 : 9, most = 40000000 / block > least ? (int)(40000000 / block) : least;
+  const int groups = (j.tiles_m + most - 1) / most;
   return (j.tiles_m + groups - 1) / groups;
 }
 
