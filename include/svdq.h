@@ -517,8 +517,9 @@ svdq_status svdq_awq_gemm(const svdq_awq_weights* w, int M, const void* X, void*
  *     elements, ld >= the row's length, ld % 8 == 0 (layer norm: any).
  *     Weights, biases, kept pre-activations (Z, G, U) and weight gradients are
  *     packed.
- *   - K, N, F > 0 and multiples of 8, M >= 0.  M == 0: a forward call is a
- *     no-op, a backward call writes zero weight and bias gradients.
+ *   - K, N, F > 0 and multiples of 8 (layer norm: C >= 1), M >= 0, each at
+ *     most 2^31 - 512.  M == 0: a forward call is a no-op, a backward call
+ *     writes zero weight and bias gradients.
  *   - Device pointers 16-byte aligned (layer norm: to their element).
  *   - Outputs overlap neither inputs nor each other, with one exception: Y
  *     may be the residual itself (same pointer, same stride).

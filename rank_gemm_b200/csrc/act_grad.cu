@@ -54,7 +54,8 @@ template <int KIND>
 __global__ void __launch_bounds__(THREADS) act_grad_kernel(ActGradParams p) {
   const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int n = blockIdx.x * COLS + cl * 8;
-  const int r0 = (int)((long long)p.M * blockIdx.y / gridDim.y), r1 = (int)((long long)p.M * (blockIdx.y + 1) / gridDim.y);
+  const int r0 = (int)((long long)p.M * blockIdx.y / gridDim.y);
+  const int r1 = (int)((long long)p.M * (blockIdx.y + 1) / gridDim.y);
   const bool fp16 = p.fp16 != 0;
   float s[8] = {}, s2[8] = {};
   grid_launch_dependents();   // the products' kernel may set up as SMs fall idle
@@ -152,15 +153,15 @@ __global__ void __launch_bounds__(32 * SUM_LANES) sum_parts_kernel(const float* 
 // second, nearly empty round cost 148 us instead of 103 for 4608 x 12288
 // gated), at least 16 rows each.
 int act_grad_parts(int M, int N) {
-  const int cb = (N + COLS - 1) / COLS;
+  const int cb = (int)(((long long)N + COLS - 1) / COLS);
   int parts = 148 * 4 / cb;
-  const int most = (M + 15) / 16;
+  const int most = (int)(((long long)M + 15) / 16);
   if (parts > most) parts = most;
   return parts < 1 ? 1 : parts;
 }
 
 cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream) {
-  const dim3 grid((p.N + COLS - 1) / COLS, p.parts);
+  const dim3 grid((unsigned)(((long long)p.N + COLS - 1) / COLS), p.parts);
   switch (p.kind) {
     case ACT_GRAD_SUM: return launch_early(act_grad_kernel<ACT_GRAD_SUM>, grid, THREADS, 0, stream, p);
     case ACT_GRAD_DENSE: return launch_early(act_grad_kernel<ACT_GRAD_DENSE>, grid, THREADS, 0, stream, p);
@@ -170,8 +171,8 @@ cudaError_t launch_act_grad(const ActGradParams& p, cudaStream_t stream) {
 
 cudaError_t launch_sum_parts(const float* part, int parts, int N, int dt, void* out, const float* part2, void* out2,
                              cudaStream_t stream) {
-  return launch_early(sum_parts_kernel, dim3((N + 31) / 32, part2 ? 2 : 1), 32 * SUM_LANES, 0, stream, part, part2, parts, N,
-                      dt, out, out2);
+  return launch_early(sum_parts_kernel, dim3((N + 31) / 32, part2 ? 2 : 1), 32 * SUM_LANES, 0, stream, part, part2,
+                      parts, N, dt, out, out2);
 }
 
 }  // namespace svdq

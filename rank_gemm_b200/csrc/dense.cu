@@ -22,7 +22,11 @@ int ceil_div(int a, int b) { return (int)(((long long)a + b - 1) / b); }
 
 bool type16(svdq_dtype dt) { return dt == SVDQ_BF16 || dt == SVDQ_FP16; }
 bool known_act(svdq_epilogue a) { return a == SVDQ_EPI_NONE || a == SVDQ_EPI_GELU_TANH || a == SVDQ_EPI_SILU; }
-bool width_ok(int n) { return n > 0 && n % 8 == 0; }
+// Sizes stay 512 short of 2^31, so that a tile's rows and columns past the
+// last still count in 32 bits.
+constexpr int MOST = 0x7FFFFE00;
+bool width_ok(int n) { return n > 0 && n % 8 == 0 && n <= MOST; }
+bool rows_ok(int m) { return m >= 0 && m <= MOST; }
 // a row stride in 16-bit elements: covers the row, 16-byte steps, under the TMA limit of 2^40 bytes
 bool stride_ok(long long ld, int width) { return ld >= width && ld % 8 == 0 && ld < (1ll << 39); }
 
@@ -289,7 +293,7 @@ svdq_status svdq_dense_linear(svdq_dtype dt, int M, int K, int N, const void* X,
                               const void* bias, svdq_epilogue act, const void* residual, long long ldr, void* Y,
                               long long ldy, void* Z, cudaStream_t stream) {
   if (!type16(dt) || !known_act(act) || !W_t || (M > 0 && (!X || !Y))) return SVDQ_ERR_INVALID_ARG;
-  if (M < 0 || !width_ok(K) || !width_ok(N) || !stride_ok(ldx, K) || !stride_ok(ldy, N) ||
+  if (!rows_ok(M) || !width_ok(K) || !width_ok(N) || !stride_ok(ldx, K) || !stride_ok(ldy, N) ||
       (residual && !stride_ok(ldr, N)))
     return SVDQ_ERR_SHAPE;
   if (!aligned16(X) || !aligned16(W_t) || !aligned16(bias) || !aligned16(residual) || !aligned16(Y) || !aligned16(Z))
@@ -309,7 +313,7 @@ svdq_status svdq_dense_linear(svdq_dtype dt, int M, int K, int N, const void* X,
 
 // [dZ when there is an activation | the bias gradient's partials]
 size_t svdq_dense_linear_backward_workspace_bytes(int M, int K, int N, svdq_epilogue act) {
-  if (M < 0 || !width_ok(K) || !width_ok(N) || !known_act(act)) return 0;
+  if (!rows_ok(M) || !width_ok(K) || !width_ok(N) || !known_act(act)) return 0;
   return (act == SVDQ_EPI_NONE ? 0 : align256((size_t)M * N * 2)) +
          align256((size_t)act_grad_parts(M, N) * N * 4);
 }
@@ -320,7 +324,7 @@ svdq_status svdq_dense_linear_backward(svdq_dtype dt, int M, int K, int N, const
                                        void* workspace, size_t ws_bytes, cudaStream_t stream) {
   if (!type16(dt) || !known_act(act)) return SVDQ_ERR_INVALID_ARG;
   if (M > 0 && (!dY || (act != SVDQ_EPI_NONE && !Z) || (dX && !W_t) || (dW && !X))) return SVDQ_ERR_INVALID_ARG;
-  if (M < 0 || !width_ok(K) || !width_ok(N) || !stride_ok(lddy, N) || (dW && !stride_ok(ldx, K)) ||
+  if (!rows_ok(M) || !width_ok(K) || !width_ok(N) || !stride_ok(lddy, N) || (dW && !stride_ok(ldx, K)) ||
       (dX && !stride_ok(lddx, K)))
     return SVDQ_ERR_SHAPE;
   if (!aligned16(dY) || !aligned16(X) || !aligned16(W_t) || !aligned16(Z) || !aligned16(dX) || !aligned16(dW) ||
@@ -371,7 +375,7 @@ svdq_status svdq_gated_linear(svdq_dtype dt, int M, int K, int F, const void* X,
                               const void* Wu_t, const void* bias_g, const void* bias_u, svdq_epilogue act, void* H,
                               long long ldh, void* G, void* U, cudaStream_t stream) {
   if (!type16(dt) || !known_act(act) || !Wg_t || !Wu_t || (M > 0 && (!X || !H))) return SVDQ_ERR_INVALID_ARG;
-  if (M < 0 || !width_ok(K) || !width_ok(F) || !stride_ok(ldx, K) || !stride_ok(ldh, F)) return SVDQ_ERR_SHAPE;
+  if (!rows_ok(M) || !width_ok(K) || !width_ok(F) || !stride_ok(ldx, K) || !stride_ok(ldh, F)) return SVDQ_ERR_SHAPE;
   if (!aligned16(X) || !aligned16(Wg_t) || !aligned16(Wu_t) || !aligned16(bias_g) || !aligned16(bias_u) ||
       !aligned16(H) || !aligned16(G) || !aligned16(U))
     return SVDQ_ERR_ALIGNMENT;
@@ -390,7 +394,7 @@ svdq_status svdq_gated_linear(svdq_dtype dt, int M, int K, int F, const void* X,
 
 // [dG | dU | the two bias gradients' partials]
 size_t svdq_gated_linear_backward_workspace_bytes(int M, int K, int F) {
-  if (M < 0 || !width_ok(K) || !width_ok(F)) return 0;
+  if (!rows_ok(M) || !width_ok(K) || !width_ok(F)) return 0;
   return 2 * align256((size_t)M * F * 2) + 2 * align256((size_t)act_grad_parts(M, F) * F * 4);
 }
 
@@ -401,7 +405,7 @@ svdq_status svdq_gated_linear_backward(svdq_dtype dt, int M, int K, int F, const
                                        size_t ws_bytes, cudaStream_t stream) {
   if (!type16(dt) || !known_act(act) || !dWg != !dWu || !dbias_g != !dbias_u) return SVDQ_ERR_INVALID_ARG;
   if (M > 0 && (!dH || !G || !U || (dX && (!Wg_t || !Wu_t)) || (dWg && !X))) return SVDQ_ERR_INVALID_ARG;
-  if (M < 0 || !width_ok(K) || !width_ok(F) || !stride_ok(lddh, F) || (dWg && !stride_ok(ldx, K)) ||
+  if (!rows_ok(M) || !width_ok(K) || !width_ok(F) || !stride_ok(lddh, F) || (dWg && !stride_ok(ldx, K)) ||
       (dX && !stride_ok(lddx, K)))
     return SVDQ_ERR_SHAPE;
   if (!aligned16(dH) || !aligned16(X) || !aligned16(Wg_t) || !aligned16(Wu_t) || !aligned16(G) || !aligned16(U) ||
@@ -461,6 +465,7 @@ static bool elem_aligned(svdq_dtype dt, const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & (elem_bytes(dt) - 1)) == 0;
 }
 static bool float_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+static bool length_ok(int C) { return C >= 1 && C <= MOST; }
 static bool known_type(svdq_dtype dt) { return dt == SVDQ_BF16 || dt == SVDQ_FP16 || dt == SVDQ_FP32; }
 
 svdq_status svdq_layernorm(svdq_dtype dt, int M, int C, const void* X, long long ldx, const void* gamma,
@@ -468,7 +473,7 @@ svdq_status svdq_layernorm(svdq_dtype dt, int M, int C, const void* X, long long
                            cudaStream_t stream) {
   if (!known_type(dt) || !gamma != !beta || (M > 0 && (!X || !Y)) || !(eps >= 0.f) || !std::isfinite(eps))
     return SVDQ_ERR_INVALID_ARG;
-  if (M < 0 || C < 1 || ldx < C || ldy < C) return SVDQ_ERR_SHAPE;
+  if (!rows_ok(M) || !length_ok(C) || ldx < C || ldy < C) return SVDQ_ERR_SHAPE;
   if (!elem_aligned(dt, X) || !elem_aligned(dt, gamma) || !elem_aligned(dt, beta) || !elem_aligned(dt, Y) ||
       !float_aligned(mean) || !float_aligned(rstd))
     return SVDQ_ERR_ALIGNMENT;
@@ -481,7 +486,8 @@ svdq_status svdq_layernorm(svdq_dtype dt, int M, int C, const void* X, long long
 
 // [dgamma partials | dbeta partials]
 size_t svdq_layernorm_backward_workspace_bytes(int M, int C) {
-  if (M < 0 || C < 1) return 0;
+  if (!rows_ok(M) || !length_ok(C)) return 0;
+  // the first 256 keep it above zero for M = 0: zero means refused
   return 256 + 2 * align256((size_t)layernorm_grad_parts(M, C) * C * 4);
 }
 
@@ -490,7 +496,7 @@ svdq_status svdq_layernorm_backward(svdq_dtype dt, int M, int C, const void* dY,
                                     long long lddx, void* dgamma, void* dbeta, void* workspace, size_t ws_bytes,
                                     cudaStream_t stream) {
   if (!known_type(dt) || !dgamma != !dbeta || (M > 0 && (!dY || !X || !mean || !rstd))) return SVDQ_ERR_INVALID_ARG;
-  if (M < 0 || C < 1 || lddy < C || ldx < C || (dX && lddx < C)) return SVDQ_ERR_SHAPE;
+  if (!rows_ok(M) || !length_ok(C) || lddy < C || ldx < C || (dX && lddx < C)) return SVDQ_ERR_SHAPE;
   if (!elem_aligned(dt, dY) || !elem_aligned(dt, X) || !elem_aligned(dt, gamma) || !elem_aligned(dt, dX) ||
       !elem_aligned(dt, dgamma) || !elem_aligned(dt, dbeta) || !float_aligned(mean) || !float_aligned(rstd) ||
       !aligned16(workspace))

@@ -229,7 +229,8 @@ __device__ __forceinline__ void fma_v(float* o, const float* a, const float* b, 
 struct Reducer {
   float (*sh)[1];   // [2][16 warps]
   int tpr, warp0, buf;
-  __device__ Reducer(float (*s)[1], int tpr_) : sh(s), tpr(tpr_), buf(0) { warp0 = (int)(threadIdx.x / tpr) * (tpr >> 5); }
+  __device__ Reducer(float (*s)[1], int tpr_)
+      : sh(s), tpr(tpr_), warp0((int)(threadIdx.x / tpr_) * (tpr_ >> 5)), buf(0) {}
   __device__ float sum1(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -306,15 +307,19 @@ struct Ring {
   }
 };
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait_oldest() { asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory"); }
+__device__ __forceinline__ void cp_wait_oldest() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+}
 
 // ------------------------------------------------------------------ forward
 // TPR threads a row, PER packs a thread, a block of several rows when a row
 // is one warp.
+template <int TPR>
+constexpr int BLOCK_OF = TPR < SMALL_BLOCK ? SMALL_BLOCK : TPR;
 template <typename T, int VEC, int TPR, int PER>
-__global__ void __launch_bounds__(TPR < SMALL_BLOCK ? SMALL_BLOCK : TPR, PER <= 4 ? 1024 / (TPR < SMALL_BLOCK ? SMALL_BLOCK : TPR) : 1)
+__global__ void __launch_bounds__(BLOCK_OF<TPR>, PER <= 4 ? 1024 / BLOCK_OF<TPR> : 1)
     layernorm_kernel(LayerNormParams p) {
-  constexpr int RPB = TPR < SMALL_BLOCK ? SMALL_BLOCK / TPR : 1;
+  constexpr int RPB = BLOCK_OF<TPR> / TPR;
   __shared__ float sh[32][1];
   extern __shared__ __align__(16) uint8_t ring_raw[];
   const int t = threadIdx.x % TPR, g0 = threadIdx.x / TPR;
@@ -668,7 +673,8 @@ template <typename T>
 __global__ void __launch_bounds__(MAX_TPR) layernorm_grad_cols_kernel(LayerNormGradParams p) {
   const int c = blockIdx.x * blockDim.x + threadIdx.x;
   if (c >= p.C) return;
-  const int r0 = (int)((long long)p.M * blockIdx.y / gridDim.y), r1 = (int)((long long)p.M * (blockIdx.y + 1) / gridDim.y);
+  const int r0 = (int)((long long)p.M * blockIdx.y / gridDim.y);
+  const int r1 = (int)((long long)p.M * (blockIdx.y + 1) / gridDim.y);
   float g = 0.f, b = 0.f;
   for (int m = r0; m < r1; ++m) {
     const float d = to_f32(static_cast<const T*>(p.dY)[(long long)m * p.lddy + c]);
@@ -716,10 +722,10 @@ constexpr int FEW_ROWS = 148 * 4;
 
 template <typename T, int VEC, int TPR, int PER>
 cudaError_t forward_as(const LayerNormParams& p, cudaStream_t st) {
-  constexpr int BLOCK = TPR < SMALL_BLOCK ? SMALL_BLOCK : TPR;
+  constexpr int BLOCK = BLOCK_OF<TPR>;
+  constexpr size_t RING = (size_t)BLOCK * Ring<typename PackOf<T, VEC>::type, PER, 1>::BYTES;
   int blocks;
-  return walk<LayerNormParams>(layernorm_kernel<T, VEC, TPR, PER>, p, BLOCK, BLOCK / TPR,
-                               (size_t)BLOCK * Ring<typename PackOf<T, VEC>::type, PER, 1>::BYTES, 1 << 30, &blocks, st);
+  return walk<LayerNormParams>(layernorm_kernel<T, VEC, TPR, PER>, p, BLOCK, BLOCK / TPR, RING, 1 << 30, &blocks, st);
 }
 
 // Up to four 16-byte packs a thread in 64 registers (1024 threads a SM): more

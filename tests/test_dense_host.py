@@ -41,7 +41,8 @@ def call(B, name, **change):
 
 
 COMMON = [(dict(dt=7), INVALID), (dict(M=-1), SHAPE)]
-PRODUCT = COMMON + [(dict(dt=2), INVALID), (dict(act=3), INVALID), (dict(act=-1), INVALID), (dict(K=0), SHAPE),
+PRODUCT = COMMON + [(dict(M=(1 << 31) - 511), SHAPE), (dict(K=(1 << 31) - 8, ldx=(1 << 31) - 8), SHAPE),
+                    (dict(dt=2), INVALID), (dict(act=3), INVALID), (dict(act=-1), INVALID), (dict(K=0), SHAPE),
                     (dict(K=-8), SHAPE), (dict(K=60), SHAPE), (dict(ldx=56), SHAPE), (dict(ldx=68), SHAPE),
                     (dict(ldx=1 << 39), SHAPE), (dict(X=P + 8), ALIGN)]
 REFUSALS = {
@@ -67,11 +68,13 @@ REFUSALS = {
     "svdq_layernorm": COMMON + [
         (dict(X=None), INVALID), (dict(Y=None), INVALID), (dict(beta=None), INVALID), (dict(gamma=None), INVALID),
         (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
-        (dict(C=0), SHAPE), (dict(ldx=32), SHAPE), (dict(ldy=32), SHAPE), (dict(X=P + 2), ALIGN),
+        (dict(C=0), SHAPE), (dict(M=(1 << 31) - 511), SHAPE), (dict(C=(1 << 31) - 511, ldx=1 << 31, ldy=1 << 31), SHAPE),
+        (dict(ldx=32), SHAPE), (dict(ldy=32), SHAPE), (dict(X=P + 2), ALIGN),
         (dict(mean=P + 2), ALIGN), (dict(dt=0, Y=P + 1), ALIGN)],
     "svdq_layernorm_backward": COMMON + [
         (dict(dY=None), INVALID), (dict(X=None), INVALID), (dict(mean=None), INVALID), (dict(rstd=None), INVALID),
-        (dict(dbeta=None), INVALID), (dict(C=0), SHAPE), (dict(lddy=32), SHAPE), (dict(ldx=32), SHAPE),
+        (dict(dbeta=None), INVALID), (dict(C=0), SHAPE), (dict(M=(1 << 31) - 511), SHAPE),
+        (dict(lddy=32), SHAPE), (dict(ldx=32), SHAPE),
         (dict(lddx=32), SHAPE), (dict(dX=P + 2), ALIGN), (dict(workspace=None), WORKSPACE),
         (dict(ws_bytes=16), WORKSPACE)],
 }
