@@ -470,7 +470,9 @@ __global__ void __launch_bounds__(MAX_TPR) layernorm_grad_kernel(LayerNormGradPa
   using RowRing = Ring<P, PER, 2 * R>;
   const RowRing ring{smem_u32(ring_raw)};
   const float inv_c = 1.0f / (float)p.C;
-  constexpr bool KEEP = PER * VEC <= 16;   // gamma in registers
+  // gamma in registers, where they hold it: 16 one-element packs of float32
+  // spill with it (4608 x 5002: 325 us, 120 without; in 16 bits 94 with it, 115)
+  constexpr bool KEEP = PER * VEC <= (VEC == 1 && sizeof(T) == 4 ? 8 : 16);
   const P* ga = static_cast<const P*>(p.gamma);
   float ag[PER][VEC], ab[PER][VEC], gam[KEEP ? PER : 1][VEC];
   grid_launch_dependents();
@@ -731,8 +733,9 @@ cudaError_t forward_as(const LayerNormParams& p, cudaStream_t st) {
 // Up to four 16-byte packs a thread in 64 registers (1024 threads a SM): more
 // values a thread share a reduction's cost, more threads hide its latency.
 // Measured, 16384 x 3072 bf16: 3 packs x 128 threads 35.5 us, 6 x 64 39.9,
-// 12 x 32 (no barrier at all, 12 warps a SM) 49.9.  One-element packs: up to
-// 16 a thread.  Few rows take fewer packs and more threads, for latency.
+// 12 x 32 (no barrier at all, 12 warps a SM) 49.9; 4608 x 3072 fp32: 3 packs
+// x 256 threads 20.8 us, 2 x 512 25.6 (one-element packs lose by 256: 4608 x
+// 3001 fp16 28.8 us for 26.5).  One-element packs: up to 16 a thread.  Few rows take fewer packs and more threads, for latency.
 template <typename T, int VEC, int TPR>
 cudaError_t forward_packs(const LayerNormParams& p, int nv, cudaStream_t st) {
   if (nv <= TPR) return forward_as<T, VEC, TPR, 1>(p, st);
@@ -751,6 +754,8 @@ cudaError_t forward(const LayerNormParams& p, cudaStream_t st) {
   const int nv = p.C / VEC, want = p.M <= FEW_ROWS ? (VEC == 1 ? 2 : 1) : MOST;   // packs a thread
   if (nv <= 32 * want) return forward_packs<T, VEC, 32>(p, nv, st);
   if (nv <= 128 * want) return forward_packs<T, VEC, 128>(p, nv, st);
+  if constexpr (VEC > 1)
+    if (nv <= 256 * want) return forward_packs<T, VEC, 256>(p, nv, st);
   if (nv <= 512 * MOST) return forward_packs<T, VEC, 512>(p, nv, st);
   if (VEC > 1 && nv <= 512 * 8) return forward_as<T, VEC, 512, 8>(p, st);
   layernorm_streamed_kernel<T, VEC><<<p.M, MAX_TPR, 0, st>>>(p);
