@@ -132,9 +132,9 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _stream(s) -> Optional[int]:
+def _stream(s, dev=None) -> Optional[int]:
     if s is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice() if dev is None else dev)
     return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
 
 
@@ -367,9 +367,12 @@ def _workspace(t, ws_bytes, dev):
 
 
 def _type_of(t, what):
-    if t is None or t.dtype not in DTYPES:
+    """(dtype, its code, the current device) for a call whose types follow t."""
+    dt = None if t is None else t.dtype
+    code = DTYPES.get(dt)
+    if code is None:
         raise ValueError("svdq: %s has to be a bfloat16, float16 or float32 tensor" % what)
-    return t.dtype, DTYPES[t.dtype], torch._C._cuda_getDevice() if t.is_cuda else -2
+    return dt, code, torch._C._cuda_getDevice() if t.is_cuda else -2
 
 
 def svdq_dense_linear(M, K, N, X, W_t, bias, act, residual, Y, Z=None, stream=None):
@@ -379,7 +382,7 @@ def svdq_dense_linear(M, K, N, X, W_t, bias, act, residual, Y, Z=None, stream=No
     y, ldy = _rows(Y, M, N, dt, dev, "Y")
     _check(lib.svdq_dense_linear(code, M, K, N, x, ldx, _flat(W_t, N * K, dt, dev, "W_t"),
                                  _flat(bias, N, dt, dev, "bias"), act, r, ldr, y, ldy,
-                                 _flat(Z, M * N, dt, dev, "Z"), _stream(stream)), "svdq_dense_linear")
+                                 _flat(Z, M * N, dt, dev, "Z"), _stream(stream, dev)), "svdq_dense_linear")
 
 
 def svdq_dense_linear_backward_workspace_bytes(M, K, N, act) -> int:
@@ -395,7 +398,7 @@ def svdq_dense_linear_backward(M, K, N, dY, X, W_t, Z, act, dX, dW, dbias, works
     _check(lib.svdq_dense_linear_backward(code, M, K, N, dy, lddy, x, ldx, _flat(W_t, N * K, dt, dev, "W_t"),
                                           _flat(Z, M * N, dt, dev, "Z"), act, dx, lddx,
                                           _flat(dW, N * K, dt, dev, "dW"), _flat(dbias, N, dt, dev, "dbias"), ws,
-                                          ws_bytes, _stream(stream)), "svdq_dense_linear_backward")
+                                          ws_bytes, _stream(stream, dev)), "svdq_dense_linear_backward")
 
 
 def svdq_gated_linear(M, K, F, X, Wg_t, Wu_t, bias_g, bias_u, act, H, G=None, U=None, stream=None):
@@ -405,7 +408,7 @@ def svdq_gated_linear(M, K, F, X, Wg_t, Wu_t, bias_g, bias_u, act, H, G=None, U=
     _check(lib.svdq_gated_linear(code, M, K, F, x, ldx, _flat(Wg_t, F * K, dt, dev, "Wg_t"),
                                  _flat(Wu_t, F * K, dt, dev, "Wu_t"), _flat(bias_g, F, dt, dev, "bias_g"),
                                  _flat(bias_u, F, dt, dev, "bias_u"), act, h, ldh, _flat(G, M * F, dt, dev, "G"),
-                                 _flat(U, M * F, dt, dev, "U"), _stream(stream)), "svdq_gated_linear")
+                                 _flat(U, M * F, dt, dev, "U"), _stream(stream, dev)), "svdq_gated_linear")
 
 
 def svdq_gated_linear_backward_workspace_bytes(M, K, F) -> int:
@@ -424,7 +427,7 @@ def svdq_gated_linear_backward(M, K, F, dH, X, Wg_t, Wu_t, G, U, act, dX, dWg, d
                                           _flat(U, M * F, dt, dev, "U"), act, dx, lddx,
                                           _flat(dWg, F * K, dt, dev, "dWg"), _flat(dWu, F * K, dt, dev, "dWu"),
                                           _flat(dbias_g, F, dt, dev, "dbias_g"),
-                                          _flat(dbias_u, F, dt, dev, "dbias_u"), ws, ws_bytes, _stream(stream)),
+                                          _flat(dbias_u, F, dt, dev, "dbias_u"), ws, ws_bytes, _stream(stream, dev)),
            "svdq_gated_linear_backward")
 
 
@@ -434,7 +437,7 @@ def svdq_layernorm(M, C, X, gamma, beta, eps, Y, mean=None, rstd=None, stream=No
     y, ldy = _rows(Y, M, C, dt, dev, "Y")
     _check(lib.svdq_layernorm(code, M, C, x, ldx, _flat(gamma, C, dt, dev, "gamma"), _flat(beta, C, dt, dev, "beta"),
                               eps, y, ldy, _flat(mean, M, torch.float32, dev, "mean"),
-                              _flat(rstd, M, torch.float32, dev, "rstd"), _stream(stream)), "svdq_layernorm")
+                              _flat(rstd, M, torch.float32, dev, "rstd"), _stream(stream, dev)), "svdq_layernorm")
 
 
 def svdq_layernorm_backward_workspace_bytes(M, C) -> int:
@@ -451,7 +454,7 @@ def svdq_layernorm_backward(M, C, dY, X, gamma, mean, rstd, dX, dgamma, dbeta, w
                                        _flat(mean, M, torch.float32, dev, "mean"),
                                        _flat(rstd, M, torch.float32, dev, "rstd"), dx, lddx,
                                        _flat(dgamma, C, dt, dev, "dgamma"), _flat(dbeta, C, dt, dev, "dbeta"), ws,
-                                       ws_bytes, _stream(stream)), "svdq_layernorm_backward")
+                                       ws_bytes, _stream(stream, dev)), "svdq_layernorm_backward")
 
 
 def svdq_norm_linear_workspace_bytes(w, M) -> int:

@@ -67,6 +67,7 @@ struct JobShape {
 // The longest share of a pair, in cycles (ca, cb a tile), as the kernel deals
 // the tiles out: `per` tiles of the second job make up for one of the first.
 long long longest_share(long long ta, long long ca, long long tb, long long cb, int per, int slots) {
+  if (!tb) return (ta + slots - 1) / slots * ca;
   const long long r = ta % slots, few = slots - r;
   const long long extra = tb && r ? std::min(tb, per * few) : 0, rest = tb - extra;
   long long most = 0;
