@@ -52,10 +52,13 @@ int clusters(int width, int num_sms) {
 // swapped 15.8, pair 15.6; 256 x 1024 -> 1024 swapped 8.6, pair 6.6.
 struct Choice {
   Gemm16Plan plan{};
+  int parts[2] = {1, 1};   // of each job's reduction
   double cycles = 0;
-  void offer(const Gemm16Plan& p, double t) {
+  void offer(const Gemm16Plan& p, double t, int parts0 = 1, int parts1 = 1) {
     if (cycles == 0 || t < cycles) {
       plan = p;
+      parts[0] = parts0;
+      parts[1] = parts1;
       cycles = t;
     }
   }
@@ -63,6 +66,7 @@ struct Choice {
 struct JobShape {
   int M, N, nk;        // output rows and columns, k-tiles
   int stacked;         // outputs stacked along the rows
+  int most_parts;      // ranges its reduction may be cut into
 };
 // The longest share of a pair, in cycles (ca, cb a tile), as the kernel deals
 // the tiles out: `per` tiles of the second job make up for one of the first.
@@ -109,11 +113,27 @@ Choice plan_pair(Gemm16Op op, JobShape a, JobShape b, int num_sms) {
     for (int s = 1; s <= (f.tall ? 1 : 4); s *= 2) {
       const int slots = clusters(2 * s, num_sms);
       if (s > 1 && ((ta && a.nk < 4 * s) || (tb && b.nk < 4 * s) || tiles > slots)) break;
-      const double share = (double)longest_share(ta, (long long)ceil_div(a.nk, s) * f.k_tile + f.tile, tb,
-                                                 (long long)ceil_div(b.nk, s) * f.k_tile + f.tile,
+      auto cost = [&](int nk) { return (long long)(grad ? gemm16_weight(nk) : nk) * f.k_tile + f.tile; };
+      const double share = (double)longest_share(ta, cost(ceil_div(a.nk, s)), tb, cost(ceil_div(b.nk, s)),
                                                  gemm16_extra(a.nk, b.nk), slots);
       best.offer({op, false, f.bn, s, f.tall},
                  f.fixed + std::max(share, std::max(arrival, stream)) + (s > 1 ? f.exchange * s : 0));
+      if (!grad || s > 1) continue;
+      // reductions cut so that every pair gets its even share, at least 8 k-tiles
+      const long long even = std::max((ta * gemm16_weight(a.nk) + tb * gemm16_weight(b.nk) + slots - 1) / slots, 8ll);
+      auto cut = [&](const JobShape& j) {
+        return j.nk ? std::max(1, std::min(j.most_parts, ceil_div(j.nk, (int)std::min<long long>(even, j.nk)))) : 1;
+      };
+      const int pa = cut(a), pb = cut(b);
+      if (pa == 1 && pb == 1) continue;
+      const int ka = ceil_div(a.nk, pa), kb = b.nk ? ceil_div(b.nk, pb) : 0;
+      const double cut_share =
+          (double)longest_share(ta * pa, cost(ka), tb * pb, cost(kb), gemm16_extra(ka, kb), slots);
+      auto floats = [](const JobShape& j, int parts) {
+        return parts > 1 ? (double)parts * j.stacked * j.M * j.N : 0.0;
+      };
+      best.offer({op, false, f.bn, 1, f.tall},
+                 f.fixed + std::max(cut_share, arrival) + 4500 + (floats(a, pa) + floats(b, pb)) * 8 / 5000, pa, pb);
     }
   }
   return best;
@@ -188,12 +208,13 @@ svdq_status forward_product(const DeviceInfo& d, svdq_dtype dt, int M, int K, in
   j.M = M;
   j.N = N;
   j.nk1 = j.nk = nk;
+  j.parts = 1;
   j.Y = out16(Y);
   j.ldy = ldy;
   Gemm16Plan plan;
   Gemm16Maps<2> maps;
   bool ok;
-  const Choice pair = plan_pair(op, {M, N, nk, 1}, {}, d.num_sms);
+  const Choice pair = plan_pair(op, {M, N, nk, 1, 1}, {}, d.num_sms);
   const Choice swapped = M <= SWAP_ROWS ? plan_swap(op, M, N, nk, d.num_sms) : Choice{};
   if (swapped.cycles > 0 && swapped.cycles < pair.cycles) {
     plan = swapped.plan;
@@ -213,6 +234,29 @@ svdq_status forward_product(const DeviceInfo& d, svdq_dtype dt, int M, int K, in
   return cuda_status(launch_gemm16(plan, maps, p, d.num_sms, stream));
 }
 
+// Ranges the reduction of an output of rows x cols may be cut into: at least 8
+// k-tiles each, at most 32 of them and 148 x 256 x 128 float32 partials.
+int most_parts(long long rows, int cols, int nk) {
+  const long long fit = 148ll * 256 * 128 / (rows * cols);
+  return (int)std::max(1ll, std::min(std::min(fit, 32ll), nk / 8ll));
+}
+// The partials' bytes in a backward pass's workspace: dX's, then dW's.
+struct PartBytes {
+  size_t dx, dw;
+};
+PartBytes part_bytes(int M, int K, int N, bool two) {
+  auto bytes = [&](long long rows, int nk) {
+    const int parts = rows ? most_parts(rows, K, nk) : 1;
+    return parts > 1 ? align256((size_t)parts * rows * K * 4) : 0;
+  };
+  return {bytes(M, ceil_div(N, 64) * (two ? 2 : 1)), bytes((long long)N * (two ? 2 : 1), ceil_div(M, 64))};
+}
+
+size_t partials_bytes(int M, int K, int N, bool two) {
+  const PartBytes b = part_bytes(M, K, N, two);
+  return b.dx + b.dw;
+}
+
 // The products of a backward pass, dZ (and dZ2) [M][N] of row stride ldz:
 //   dW [N][K] = dZ^T X, dW2 = dZ2^T X (stacked below it)   when dW
 //   dX [M][K] = dZ W + dZ2 W2                              when dX
@@ -222,6 +266,7 @@ struct Backward {
   const void *dZ, *dZ2, *X, *W, *W2;
   long long ldz, ldx, lddx;
   void *dX, *dW, *dW2;
+  uint8_t* partials;   // part_bytes
 };
 svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward& g, Gemm16Params p,
                               cudaStream_t stream) {
@@ -241,7 +286,8 @@ svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward
     j.Y = out16(g.dW);
     j.Y2 = out16(g.dW2);
     j.ldy = g.K;
-    shape[at_w] = {g.N, g.K, j.nk, two ? 2 : 1};
+    j.P = reinterpret_cast<float*>(g.partials + part_bytes(g.M, g.K, g.N, two).dx);
+    shape[at_w] = {g.N, g.K, j.nk, two ? 2 : 1, most_parts((long long)g.N * (two ? 2 : 1), g.K, j.nk)};
   }
   if (g.dX) {
     at_x = jobs++;
@@ -252,7 +298,8 @@ svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward
     j.nk = two ? 2 * j.nk1 : j.nk1;
     j.Y = out16(g.dX);
     j.ldy = g.lddx;
-    shape[at_x] = {g.M, g.K, j.nk, 1};
+    j.P = reinterpret_cast<float*>(g.partials);
+    shape[at_x] = {g.M, g.K, j.nk, 1, most_parts(g.M, g.K, j.nk)};
   }
   if (!jobs) return SVDQ_OK;
   if (jobs == 2 && p.job[1].nk > p.job[0].nk) {   // the longer tiles first
@@ -265,11 +312,13 @@ svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward
     at_w ^= 1;
     at_x ^= 1;
   }
-  const Gemm16Plan plan = plan_pair(GEMM16_GRAD, shape[0], shape[1], d.num_sms).plan;
+  const Choice choice = plan_pair(GEMM16_GRAD, shape[0], shape[1], d.num_sms);
+  const Gemm16Plan& plan = choice.plan;
   for (int i = 0; i < jobs; ++i) {
     p.job[i].tiles_n = ceil_div(g.K, plan.bn);
     p.job[i].tiles_m1 = ceil_div(shape[i].M, plan.tall ? 512 : 256);
     p.job[i].tiles_m = shape[i].stacked * p.job[i].tiles_m1;
+    p.job[i].parts = choice.parts[i];
   }
   Gemm16Maps<2> maps;
   if (at_w >= 0 &&
@@ -282,7 +331,12 @@ svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward
     for (int i = 0; i < MAPS; ++i) maps.m[1][i] = maps.m[0][i];
   p.fp16 = dt == SVDQ_FP16;
   p.err = d.err;
-  return cuda_status(launch_gemm16(plan, maps, p, d.num_sms, stream));
+  const svdq_status s = cuda_status(launch_gemm16(plan, maps, p, d.num_sms, stream));
+  Gemm16Job cut[2];
+  int cuts = 0;
+  for (int i = 0; i < jobs; ++i)
+    if (p.job[i].parts > 1) cut[cuts++] = p.job[i];
+  return s != SVDQ_OK || !cuts ? s : cuda_status(launch_join_parts(cut, cuts, p.fp16, stream));
 }
 
 cudaError_t zero(void* p, size_t bytes, cudaStream_t stream) {
@@ -316,11 +370,11 @@ svdq_status svdq_dense_linear(svdq_dtype dt, int M, int K, int N, const void* X,
   return forward_product(d, dt, M, K, N, X, ldx, W_t, nullptr, Y, ldy, p, stream);
 }
 
-// [dZ when there is an activation | the bias gradient's partials]
+// [dZ when there is an activation | the bias gradient's partials | the products' partials]
 size_t svdq_dense_linear_backward_workspace_bytes(int M, int K, int N, svdq_epilogue act) {
   if (!rows_ok(M) || !width_ok(K) || !width_ok(N) || !known_act(act)) return 0;
   return (act == SVDQ_EPI_NONE ? 0 : align256((size_t)M * N * 2)) +
-         align256((size_t)act_grad_parts(M, N) * N * 4);
+         align256((size_t)act_grad_parts(M, N) * N * 4) + partials_bytes(M, K, N, false);
 }
 
 svdq_status svdq_dense_linear_backward(svdq_dtype dt, int M, int K, int N, const void* dY, long long lddy,
@@ -372,7 +426,9 @@ svdq_status svdq_dense_linear_backward(svdq_dtype dt, int M, int K, int N, const
   }
   const void* dZ = has_act ? workspace : dY;
   const long long ldz = has_act ? N : lddy;
-  return backward_products(d, dt, {M, K, N, dZ, nullptr, X, W_t, nullptr, ldz, ldx, lddx, dX, dW, nullptr}, q, stream);
+  uint8_t* partials = reinterpret_cast<uint8_t*>(part) + align256((size_t)act_grad_parts(M, N) * N * 4);
+  return backward_products(d, dt, {M, K, N, dZ, nullptr, X, W_t, nullptr, ldz, ldx, lddx, dX, dW, nullptr, partials}, q,
+                           stream);
 }
 
 // ------------------------------------------------------------------ gated feed-forward
@@ -397,10 +453,11 @@ svdq_status svdq_gated_linear(svdq_dtype dt, int M, int K, int F, const void* X,
   return forward_product(d, dt, M, K, F, X, ldx, Wg_t, Wu_t, H, ldh, p, stream);
 }
 
-// [dG | dU | the two bias gradients' partials]
+// [dG | dU | the two bias gradients' partials | the products' partials]
 size_t svdq_gated_linear_backward_workspace_bytes(int M, int K, int F) {
   if (!rows_ok(M) || !width_ok(K) || !width_ok(F)) return 0;
-  return 2 * align256((size_t)M * F * 2) + 2 * align256((size_t)act_grad_parts(M, F) * F * 4);
+  return 2 * align256((size_t)M * F * 2) + 2 * align256((size_t)act_grad_parts(M, F) * F * 4) +
+         partials_bytes(M, K, F, true);
 }
 
 svdq_status svdq_gated_linear_backward(svdq_dtype dt, int M, int K, int F, const void* dH, long long lddh,
@@ -461,7 +518,9 @@ svdq_status svdq_gated_linear_backward(svdq_dtype dt, int M, int K, int F, const
     q.dbias = out16(dbias_g);
     q.dbias2 = out16(dbias_u);
   }
-  return backward_products(d, dt, {M, K, F, p.dZ, p.dU, X, Wg_t, Wu_t, F, ldx, lddx, dX, dWg, dWu}, q, stream);
+  uint8_t* partials = reinterpret_cast<uint8_t*>(part2) + align256((size_t)p.parts * F * 4);
+  return backward_products(
+      d, dt, {M, K, F, p.dZ, p.dU, X, Wg_t, Wu_t, F, ldx, lddx, dX, dWg, dWu, partials}, q, stream);
 }
 
 // ------------------------------------------------------------------ layer norm

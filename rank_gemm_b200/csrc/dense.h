@@ -65,6 +65,10 @@ struct Gemm16Job {
   int a_mn;                    // GRAD: A has the reduction index outermost
   uint16_t *Y, *Y2;            // output rows of stride ldy; the second stacked output
   long long ldy;
+  // GRAD: the reduction in `parts` ranges of k-tiles, a tile each.  More than
+  // one: float32 partials P [parts][rows of Y, of Y2][N] instead of Y and Y2.
+  int parts;
+  float* P;
 };
 struct Gemm16Params {
   Gemm16Job job[2];            // the second: GRAD only
@@ -88,10 +92,17 @@ template <int JOBS>
 struct Gemm16Maps {
   CUtensorMap m[JOBS][MAPS];
 };
+// A tile's epilogue takes as long as about seven k-tiles (40 x 7840 -> 5232
+// backward, whose dW tiles have one: counted as one 147 us, as seven 46).
+constexpr int gemm16_weight(int nk) { return nk > 7 ? nk : 7; }
 // Tiles of the second job that make up for one of the first.
-constexpr int gemm16_extra(int nk0, int nk1) { return nk1 > 0 ? (nk0 + nk1 / 2) / nk1 : 0; }
+constexpr int gemm16_extra(int nk0, int nk1) {
+  return nk1 > 0 ? (gemm16_weight(nk0) + gemm16_weight(nk1) / 2) / gemm16_weight(nk1) : 0;
+}
 // Columns of the pair form's store boxes (32 rows high; 128-byte swizzle, 64-byte for 32 columns).
 constexpr int gemm16_box_cols(const Gemm16Plan& p) { return p.op == GEMM16_GATED && p.bn == 128 ? 32 : 64; }
+// Y (and Y2) = the sum of a job's partials, in order, rounded once; of one or two jobs.
+cudaError_t launch_join_parts(const Gemm16Job* jobs, int count, int fp16, cudaStream_t stream);
 cudaError_t launch_gemm16(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, Gemm16Params p, int num_sms,
                           cudaStream_t stream);
 

@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
 
   // this pair (CTA, cluster), of how many
   const int first = (int)blockIdx.x / (CG * S), slots = (int)gridDim.x / (CG * S);
-  const int tiles0 = p.job[0].tiles_m * p.job[0].tiles_n, tiles1 = GRAD ? p.job[1].tiles_m * p.job[1].tiles_n : 0;
+  auto tiles_of = [&](const Gemm16Job& j) { return j.tiles_m * j.tiles_n * (GRAD ? j.parts : 1); };
+  const int tiles0 = tiles_of(p.job[0]), tiles1 = GRAD ? tiles_of(p.job[1]) : 0;
   // The n-th tile of this pair: its job and block coordinates.  Job 0's tiles
   // go round the pairs; the pairs left with one fewer of them take
   // job1_extra tiles of job 1 each, and the rest of job 1 goes round from the
@@ -361,6 +362,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
     bool valid;
     int job, mb, nb;
     bool second;   // of two stacked A operands and outputs; mb counts within it
+    int part;      // range of the reduction
   };
   auto tile_at = [&](int n) {
     Tile t;
@@ -377,6 +379,8 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
     }
     if (t.valid) {
       const Gemm16Job& j = p.job[t.job];
+      t.part = GRAD && j.parts > 1 ? tile / (j.tiles_m * j.tiles_n) : 0;
+      if (GRAD) tile -= t.part * j.tiles_m * j.tiles_n;
       const int per = j.group * j.tiles_n, g = tile / per, q = tile - g * per;
       const int rows = min(j.group, j.tiles_m - g * j.group);
       t.mb = g * j.group + q % rows;
@@ -386,8 +390,10 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
     }
     return t;
   };
-  auto k_begin = [&](const Gemm16Job& j) { return (int)((long long)j.nk * split / S); };
-  auto k_end = [&](const Gemm16Job& j) { return (int)((long long)j.nk * (split + 1) / S); };
+  // its k-tiles: one range of a cluster's CTAs, or of the job's parts
+  auto k_at = [&](const Gemm16Job& j, int i) { return (int)((long long)j.nk * i / (GRAD ? S * j.parts : S)); };
+  auto k_begin = [&](const Gemm16Job& j, const Tile& t) { return k_at(j, t.part * S + split); };
+  auto k_end = [&](const Gemm16Job& j, const Tile& t) { return k_at(j, t.part * S + split + 1); };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -409,8 +415,8 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
         const bool a_mn = GRAD && j.a_mn;
         const int a_row = t.mb * C::TILE_ROWS + cta * 128;
         const int b_row = (GATED && !SWAP) ? t.nb * OUT_COLS : t.nb * BN + cta * C::B_ROWS;
-        const int kt1 = k_end(j);
-        for (int k0 = k_begin(j); k0 < kt1; k0 += C::KS, next()) {
+        const int kt1 = k_end(j, t);
+        for (int k0 = k_begin(j, t); k0 < kt1; k0 += C::KS, next()) {
           if (!(ok = mbar_wait(smem_u32(&ctl->empty[stage]), phase ^ 1, abort_flag, p.err))) break;
           const uint32_t bar = smem_u32(&ctl->full[stage]);
           const uint32_t sig = CG == 2 ? dsmem_map(bar, rank & ~1u) : bar;
@@ -481,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
         const Gemm16Job& job = p.job[tile.job];
         const bool a_mn = GRAD && job.a_mn;
         const uint32_t idesc = idesc0 | (a_mn ? 1u << 15 : 0u);
-        const int nk = k_end(job) - k_begin(job);
+        const int nk = k_end(job, tile) - k_begin(job, tile);
         // the k-tiles of the stage at x, `left` of the tile's, into accumulators [T0, T1) at column acc
         auto multiply = [&](const Slot& x, uint32_t acc, auto t0, auto t1, int left, bool first_k) {
           constexpr int T0 = decltype(t0)::value, T1 = decltype(t1)::value;
@@ -688,11 +694,26 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
         __syncwarp();
         if (lane == 0 && row_w < j.M && n_tile + c < j.N) tma_store_2d(map + at, box, n_tile + c, row_w);
       };
+      // A part of the reduction: the accumulators as they are.
+      if (GRAD && j.parts > 1) {
+        float* dst = j.P + ((size_t)(t.part * (j.Y2 ? 2 : 1) + (second ? 1 : 0)) * j.M + m) * j.N;
 #pragma unroll 1
-      for (int c = c0; c < c0 + PER; c += W) {
-        if (!GRAD && p.Z) emit_box(OUT_Z, MAP_Z, c);
-        if (GATED && p.Z2) emit_box(OUT_Z2, MAP_Z2, c);
-        emit_box(OUT_Y, second ? MAP_Y2 : MAP_Y, c);
+        for (int c = c0; c < c0 + PER; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(taddr + c, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            if (m < j.M && n_tile + c + i < j.N)
+              *reinterpret_cast<uint4*>(dst + n_tile + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = c0; c < c0 + PER; c += W) {
+          if (!GRAD && p.Z) emit_box(OUT_Z, MAP_Z, c);
+          if (GATED && p.Z2) emit_box(OUT_Z2, MAP_Z2, c);
+          emit_box(OUT_Y, second ? MAP_Y2 : MAP_Y, c);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -876,14 +897,46 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
 
 namespace {
 
+// ------------------------------------------------------------------ joining the parts of a reduction
+// Eight columns a thread, the parts in order: no atomics, the same bits on
+// every run.  Bound by latency: the partials, at most 19 MB, come from L2.
+struct JoinParams {
+  struct {
+    const float* P;
+    uint16_t *Y, *Y2;
+    long long ldy;
+    int M, N, parts;
+  } job[2];
+};
+template <bool FP16>
+__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ JoinParams p) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const auto& j = p.job[blockIdx.y];
+  const int per_row = j.N / 8, rows = j.M * (j.Y2 ? 2 : 1);
+  const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (at >= (long long)rows * per_row) return;
+  const int row = (int)(at / per_row), col = (int)(at - (long long)row * per_row) * 8;
+  const float* src = j.P + (size_t)row * j.N + col;
+  float v[8] = {};
+#pragma unroll 4
+  for (int s = 0; s < j.parts; ++s, src += (size_t)rows * j.N) {
+    const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  }
+  uint16_t* y = row < j.M ? j.Y + (size_t)row * j.ldy : j.Y2 + (size_t)(row - j.M) * j.ldy;
+  store8(y + col, v, FP16);
+}
+
 template <int CG, int BN, bool SWAP, bool GATED, bool GRAD, bool TALL, bool FP16>
 cudaError_t launch(const Gemm16Maps<2>& maps, const Gemm16Params& p, int num_sms, cudaStream_t stream) {
   using C = Cfg<CG, BN, SWAP, GATED, TALL>;
   auto kern = gemm16_kernel<CG, BN, SWAP, GATED, GRAD, TALL, FP16>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
-  const long long tiles =
-      (long long)p.job[0].tiles_m * p.job[0].tiles_n + (long long)p.job[1].tiles_m * p.job[1].tiles_n;
+  long long tiles = 0;
+  for (const Gemm16Job& j : p.job) tiles += (long long)j.tiles_m * j.tiles_n * j.parts;
   const int width = CG * p.splits;
   const long long most = p.splits > 1 ? tiles : num_sms / CG;   // a split cluster owns one tile
   cudaLaunchConfig_t cfg = {};
@@ -964,6 +1017,20 @@ cudaError_t launch_gemm16(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, Gem
   p.job[1].group = group_rows(p.job[1], plan.tall);
   p.job1_extra = gemm16_extra(p.job[0].nk, p.job[1].nk);
   return p.fp16 ? launch_as<true>(plan, maps, p, num_sms, stream) : launch_as<false>(plan, maps, p, num_sms, stream);
+}
+
+cudaError_t launch_join_parts(const Gemm16Job* jobs, int count, int fp16, cudaStream_t stream) {
+  JoinParams q = {};
+  long long most = 0;
+  for (int i = 0; i < count; ++i) {
+    const Gemm16Job& j = jobs[i];
+    const long long chunks = (long long)j.M * (j.Y2 ? 2 : 1) * (j.N / 8);
+    q.job[i] = {j.P, j.Y, j.Y2, j.ldy, j.M, j.N, j.parts};
+    if (chunks > most) most = chunks;
+  }
+  const dim3 grid((unsigned)((most + 255) / 256), count);
+  return fp16 ? launch_early(join_parts_kernel<true>, grid, 256, 0, stream, q)
+              : launch_early(join_parts_kernel<false>, grid, 256, 0, stream, q);
 }
 
 }  // namespace svdq

@@ -341,3 +341,46 @@ def test_layernorm_backward(B, t, M, C, pad, affine):
         assert bool(dX[:, C:].isnan().all())
     close(db, dy.sum(0), M * S32 * dy.abs().sum(0), "dbeta")
     close(dg, (dy * xh).sum(0), (M + 2) * S32 * (dy * xh).abs().sum(0) + (dy.abs() * xb).sum(0), "dgamma")
+
+
+# ---------------------------------------------------------------- long reductions over few tiles
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,K,N", [(5, 96, 9408), (1, 8, 4104), (7002, 80, 64), (2500, 72, 2824), (40, 2056, 5232),
+                                   (700, 1024, 4096), (16392, 264, 136)])
+def test_linear_backward_reduction_in_parts(B, t, M, K, N):
+    run_linear_backward(B, t, M, K, N, "none")
+
+
+@pytest.mark.parametrize("want", [("dX",), ("dW",), ("dX", "db"), ("dX", "dW")])
+def test_linear_backward_reduction_in_parts_one_product(B, want):
+    run_linear_backward(B, torch.bfloat16, 4100, 136, 4104, "silu", pad=16, want=want)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,K,F", [(2, 752, 5856), (6241, 88, 1544), (130, 264, 2056)])
+def test_gated_backward_reduction_in_parts(B, t, M, K, F):
+    test_gated_backward(B, t, M, K, F, "silu")
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,K,N", [(5, 96, 9408), (4100, 136, 4104), (2, 752, 5856), (300, 264, 520)])
+def test_backward_workspace_is_enough(B, gated, M, K, N):
+    """Nothing behind the stated bytes is written, and the same bits come out on every run."""
+    g, t = gen(9), torch.bfloat16
+    X, dY, W, W2, Z, U = (draw(g, t, *s) for s in ((M, K), (M, N), (N, K), (N, K), (M, N), (M, N)))
+    size = B.svdq_gated_linear_backward_workspace_bytes(M, K, N) if gated else \
+        B.svdq_dense_linear_backward_workspace_bytes(M, K, N, 2)
+    runs = []
+    for fill in (255, 0):
+        ws = torch.full((size + 4096,), fill, dtype=torch.uint8, device="cuda")
+        dX, dW, dW2, db, db2 = (nan_like(t, *s) for s in ((M, K), (N, K), (N, K), (N,), (N,)))
+        if gated:
+            B.svdq_gated_linear_backward(M, K, N, dY, X, W, W2, Z, U, 2, dX, dW, dW2, db, db2, ws, size)
+            runs.append((dX, dW, dW2, db, db2))
+        else:
+            B.svdq_dense_linear_backward(M, K, N, dY, X, W, Z, 2, dX, dW, db, ws, size)
+            runs.append((dX, dW, db))
+        torch.cuda.synchronize()
+        assert bool((ws[size:] == fill).all())
+    for a, b in zip(*runs):
+        assert bool(a.isfinite().all()) and torch.equal(a, b)
