@@ -119,7 +119,10 @@ Choice plan_pair(Gemm16Op op, JobShape a, JobShape b, int num_sms) {
       best.offer({op, false, f.bn, s, f.tall},
                  f.fixed + std::max(share, std::max(arrival, stream)) + (s > 1 ? f.exchange * s : 0));
       if (!grad || s > 1) continue;
-      // reductions cut so that every pair gets its even share, at least 8 k-tiles
+      // Reductions cut so that every pair gets its even share, at least 8
+      // k-tiles: float32 partials and a kernel that joins them, 9000 cycles
+      // (7 x 96 -> 3168 backward 15.6 us, cut 8.1; 8192 x 512 -> 512 35.0,
+      // cut 16.7; counted as 4500: 128 x 1024 -> 1024 8.0, cut 8.8).
       const long long even = std::max((ta * gemm16_weight(a.nk) + tb * gemm16_weight(b.nk) + slots - 1) / slots, 8ll);
       auto cut = [&](const JobShape& j) {
         return j.nk ? std::max(1, std::min(j.most_parts, ceil_div(j.nk, (int)std::min<long long>(even, j.nk)))) : 1;
@@ -133,7 +136,7 @@ Choice plan_pair(Gemm16Op op, JobShape a, JobShape b, int num_sms) {
         return parts > 1 ? (double)parts * j.stacked * j.M * j.N : 0.0;
       };
       best.offer({op, false, f.bn, 1, f.tall},
-                 f.fixed + std::max(cut_share, arrival) + 4500 + (floats(a, pa) + floats(b, pb)) * 8 / 5000, pa, pb);
+                 f.fixed + std::max(cut_share, arrival) + 9000 + (floats(a, pa) + floats(b, pb)) * 8 / 5000, pa, pb);
     }
   }
   return best;
@@ -158,6 +161,9 @@ Choice plan_swap(Gemm16Op op, int tokens, int features, int nk, int num_sms) {
 }
 // More rows of X than this never gain from the swapped form.
 constexpr int SWAP_ROWS = 256;
+// Up to this many rows the pair form never gains: its 256-row boxes, nearly
+// empty, come slower than full ones (gated 2 x 1272 -> 4344: 12.7 us, swapped 9.1).
+constexpr int PAIR_ROWS = 32;
 
 // ------------------------------------------------------------------ operands
 struct Operand {
@@ -168,6 +174,8 @@ CUtensorMapDataType map_type(svdq_dtype dt) {
   return dt == SVDQ_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
 
+// Rows of one part's partials: whole store boxes, so that none reaches into the next part.
+long long part_rows(int M, int stacked) { return ((long long)M + 31) / 32 * 32 * stacked; }
 // A job's maps: operands in boxes of 64 along their inner extent, outputs in
 // the epilogue's store boxes.
 bool encode_job(const Gemm16Plan& plan, svdq_dtype dt, const Operand& a, const Operand* a2, const Operand& b,
@@ -185,7 +193,13 @@ bool encode_job(const Gemm16Plan& plan, svdq_dtype dt, const Operand& a, const O
   auto out = [&](CUtensorMap* to, void* ptr, uint64_t ld) {
     return encode_tensor_map_2d(to, t, ptr, j.N, j.M, ld * 2, cols, rows, swz);
   };
-  if (!in(&m[MAP_A], a, a_box) || !in(&m[MAP_B], b, b_box) || !out(&m[MAP_Y], j.Y, j.ldy)) return false;
+  auto partials = [&](CUtensorMap* to) {
+    return encode_tensor_map_2d(to, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, j.P, j.N,
+                                j.parts * part_rows(j.M, j.Y2 ? 2 : 1), (uint64_t)j.N * 4, 32, 32,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (!in(&m[MAP_A], a, a_box) || !in(&m[MAP_B], b, b_box)) return false;
+  if (!(j.parts > 1 ? partials(&m[MAP_Y]) : out(&m[MAP_Y], j.Y, j.ldy))) return false;
   m[MAP_A2] = m[MAP_A];
   m[MAP_B2] = m[MAP_B];
   m[MAP_Z] = m[MAP_Z2] = m[MAP_Y];
@@ -216,7 +230,7 @@ svdq_status forward_product(const DeviceInfo& d, svdq_dtype dt, int M, int K, in
   bool ok;
   const Choice pair = plan_pair(op, {M, N, nk, 1, 1}, {}, d.num_sms);
   const Choice swapped = M <= SWAP_ROWS ? plan_swap(op, M, N, nk, d.num_sms) : Choice{};
-  if (swapped.cycles > 0 && swapped.cycles < pair.cycles) {
+  if (M <= PAIR_ROWS || (swapped.cycles > 0 && swapped.cycles < pair.cycles)) {
     plan = swapped.plan;
     j.tiles_m = ceil_div(N, 128);
     j.tiles_n = ceil_div(M, plan.bn);
@@ -237,7 +251,7 @@ svdq_status forward_product(const DeviceInfo& d, svdq_dtype dt, int M, int K, in
 // Ranges the reduction of an output of rows x cols may be cut into: at least 8
 // k-tiles each, at most 32 of them and 148 x 256 x 128 float32 partials.
 int most_parts(long long rows, int cols, int nk) {
-  const long long fit = 148ll * 256 * 128 / (rows * cols);
+  const long long fit = 148ll * 256 * 128 / (rows * cols);   // rows: of the partials
   return (int)std::max(1ll, std::min(std::min(fit, 32ll), nk / 8ll));
 }
 // The partials' bytes in a backward pass's workspace: dX's, then dW's.
@@ -249,7 +263,7 @@ PartBytes part_bytes(int M, int K, int N, bool two) {
     const int parts = rows ? most_parts(rows, K, nk) : 1;
     return parts > 1 ? align256((size_t)parts * rows * K * 4) : 0;
   };
-  return {bytes(M, ceil_div(N, 64) * (two ? 2 : 1)), bytes((long long)N * (two ? 2 : 1), ceil_div(M, 64))};
+  return {bytes(part_rows(M, 1), ceil_div(N, 64) * (two ? 2 : 1)), bytes(part_rows(N, two ? 2 : 1), ceil_div(M, 64))};
 }
 
 size_t partials_bytes(int M, int K, int N, bool two) {
@@ -287,7 +301,7 @@ svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward
     j.Y2 = out16(g.dW2);
     j.ldy = g.K;
     j.P = reinterpret_cast<float*>(g.partials + part_bytes(g.M, g.K, g.N, two).dx);
-    shape[at_w] = {g.N, g.K, j.nk, two ? 2 : 1, most_parts((long long)g.N * (two ? 2 : 1), g.K, j.nk)};
+    shape[at_w] = {g.N, g.K, j.nk, two ? 2 : 1, most_parts(part_rows(g.N, two ? 2 : 1), g.K, j.nk)};
   }
   if (g.dX) {
     at_x = jobs++;
@@ -299,7 +313,7 @@ svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward
     j.Y = out16(g.dX);
     j.ldy = g.lddx;
     j.P = reinterpret_cast<float*>(g.partials);
-    shape[at_x] = {g.M, g.K, j.nk, 1, most_parts(g.M, g.K, j.nk)};
+    shape[at_x] = {g.M, g.K, j.nk, 1, most_parts(part_rows(g.M, 1), g.K, j.nk)};
   }
   if (!jobs) return SVDQ_OK;
   if (jobs == 2 && p.job[1].nk > p.job[0].nk) {   // the longer tiles first

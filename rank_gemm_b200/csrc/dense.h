@@ -66,7 +66,8 @@ struct Gemm16Job {
   uint16_t *Y, *Y2;            // output rows of stride ldy; the second stacked output
   long long ldy;
   // GRAD: the reduction in `parts` ranges of k-tiles, a tile each.  More than
-  // one: float32 partials P [parts][rows of Y, of Y2][N] instead of Y and Y2.
+  // one: float32 partials P [parts][rows of Y, of Y2][N] instead of Y and Y2,
+  // the rows of each rounded up to 32.
   int parts;
   float* P;
 };

@@ -42,7 +42,10 @@
 // by the epilogue warps before their first tile.
 // Few tiles: the reduction is split over the CTAs of a cluster, whose float32
 // partial tiles are summed in rank order through distributed shared memory
-// (no workspace, no atomics, the same bits on every run).
+// (no workspace, no atomics, the same bits on every run).  A backward
+// product of few tiles and a long reduction (few rows, or many rows of narrow
+// layers) is cut into up to 32 parts that are tiles of their own: float32
+// partials in the workspace, joined in order by join_parts_kernel.
 // Outputs of whole tiles leave through shared memory, a 32-row box of 128-byte
 // rows per warp (swapped: one box of 128 features) and TMA store, so they
 // reach L2 as full lines.
@@ -694,18 +697,25 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
         __syncwarp();
         if (lane == 0 && row_w < j.M && n_tile + c < j.N) tma_store_2d(map + at, box, n_tile + c, row_w);
       };
-      // A part of the reduction: the accumulators as they are.
+      // A part of the reduction: the accumulators as they are, 32 columns a box.
       if (GRAD && j.parts > 1) {
-        float* dst = j.P + ((size_t)(t.part * (j.Y2 ? 2 : 1) + (second ? 1 : 0)) * j.M + m) * j.N;
+        const int below = (t.part * (j.Y2 ? 2 : 1) + (second ? 1 : 0)) * ((j.M + 31) / 32 * 32);
 #pragma unroll 1
-        for (int c = c0; c < c0 + PER; c += 16) {
-          uint32_t r[16];
-          tmem_ld16(taddr + c, r);
+        for (int c = c0; c < c0 + PER; c += 32) {
+          uint32_t r[2][16];
+          tmem_ld16(taddr + c, r[0]);
+          tmem_ld16(taddr + c + 16, r[1]);
+          if (lane == 0) bulk_wait_read();   // the previous box has left shared memory
+          __syncwarp();
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            if (m < j.M && n_tile + c + i < j.N)
-              *reinterpret_cast<uint4*>(dst + n_tile + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t* v = &r[i >> 2][4 * (i & 3)];
+            sts128(box + lane * 128 + ((i ^ (lane & 7)) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row_w < j.M && n_tile + c < j.N) tma_store_2d(map + MAP_Y, box, n_tile + c, below + row_w);
         }
       } else {
 #pragma unroll 1
@@ -899,7 +909,7 @@ namespace {
 
 // ------------------------------------------------------------------ joining the parts of a reduction
 // Eight columns a thread, the parts in order: no atomics, the same bits on
-// every run.  Bound by latency: the partials, at most 19 MB, come from L2.
+// every run.  Bound by latency: the partials, at most 20 MB, come from L2.
 struct JoinParams {
   struct {
     const float* P;
@@ -913,19 +923,21 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__
   grid_launch_dependents();
   grid_dependency_wait();
   const auto& j = p.job[blockIdx.y];
-  const int per_row = j.N / 8, rows = j.M * (j.Y2 ? 2 : 1);
+  const int per_row = j.N / 8, rows = j.M * (j.Y2 ? 2 : 1), pad = (j.M + 31) / 32 * 32;   // of each stacked output
   const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
   if (at >= (long long)rows * per_row) return;
   const int row = (int)(at / per_row), col = (int)(at - (long long)row * per_row) * 8;
-  const float* src = j.P + (size_t)row * j.N + col;
+  const bool second = row >= j.M;
+  const float* src = j.P + (size_t)(second ? row - j.M + pad : row) * j.N + col;
   float v[8] = {};
 #pragma unroll 4
-  for (int s = 0; s < j.parts; ++s, src += (size_t)rows * j.N) {
+  for (int s = 0; s < j.parts; ++s, src += (size_t)pad * (j.Y2 ? 2 : 1) * j.N) {
     const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
-    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    const float part[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += part[i];
   }
-  uint16_t* y = row < j.M ? j.Y + (size_t)row * j.ldy : j.Y2 + (size_t)(row - j.M) * j.ldy;
+  uint16_t* y = second ? j.Y2 + (size_t)(row - j.M) * j.ldy : j.Y + (size_t)row * j.ldy;
   store8(y + col, v, FP16);
 }
 
