@@ -1027,7 +1027,8 @@ cudaError_t launch_gemm16(const Gemm16Plan& plan, const Gemm16Maps<2>& maps, Gem
   p.splits = plan.splits;
   p.job[0].group = group_rows(p.job[0], plan.tall);
   p.job[1].group = group_rows(p.job[1], plan.tall);
-  p.job1_extra = gemm16_extra(p.job[0].nk, p.job[1].nk);
+  auto tile_nk = [](const Gemm16Job& j) { return j.parts ? (j.nk + j.parts - 1) / j.parts : 0; };
+  p.job1_extra = gemm16_extra(tile_nk(p.job[0]), tile_nk(p.job[1]));
   return p.fp16 ? launch_as<true>(plan, maps, p, num_sms, stream) : launch_as<false>(plan, maps, p, num_sms, stream);
 }
 
