@@ -209,7 +209,7 @@ def same(a, b):
         assert torch.equal(a[k], b[k]), k
 
 
-SHAPES = [(1, 256, 384), (40, 1024, 512), (333, 264, 520), (700, 512, 264)]
+SHAPES = [(1, 256, 384), (40, 1024, 512), (333, 264, 520), (700, 512, 264), (5, 96, 4104), (4100, 136, 96)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
