@@ -779,9 +779,11 @@ cudaError_t forward(const LayerNormParams& p, cudaStream_t st) {
 // 16384 x 3072 bf16 with the weights' gradients: 61.0 us, one row a round
 // 65.4, two packs and one row 63.4, two packs and two rows, which leave room
 // for fewer threads, 98.8), more packs and one row a round for longer rows.
+// Eight one-element packs: one row (8192 x 1001 fp16 25.9, two 27.4; 900 x 3001
+// 12.4, 14.1; 4608 x 3001 49.8, 46.3).
 template <typename T, int VEC, int PER>
 cudaError_t backward_as(const LayerNormGradParams& p, int most, int* parts, cudaStream_t st) {
-  constexpr int R = PER * VEC <= 8 ? 2 : 1;
+  constexpr int R = PER * VEC <= (VEC == 1 ? 4 : 8) ? 2 : 1;
   const int nv = p.C / VEC, tpr = ((nv + PER - 1) / PER + 31) / 32 * 32;
   const int block = tpr >= SMALL_BLOCK ? tpr : SMALL_BLOCK / tpr * tpr;
   const size_t ring = (size_t)block * Ring<typename PackOf<T, VEC>::type, PER, 2 * R>::BYTES;
