@@ -747,7 +747,8 @@ cudaError_t forward_as(const LayerNormParams& p, cudaStream_t st) {
 // Measured, 16384 x 3072 bf16: 3 packs x 128 threads 35.5 us, 6 x 64 39.9,
 // 12 x 32 (no barrier at all, 12 warps a SM) 49.9; 4608 x 3072 fp32: 3 packs
 // x 256 threads 20.8 us, 2 x 512 25.6 (one-element packs lose by 256: 4608 x
-// 3001 fp16 28.8 us for 26.5).  One-element packs: up to 16 a thread.  Few rows take fewer packs and more threads, for latency.
+// 3001 fp16 28.8 us for 26.5).  One-element packs: up to 16 a thread.  Few rows
+// take fewer packs and more threads, for latency.
 template <typename T, int VEC, int TPR>
 cudaError_t forward_packs(const LayerNormParams& p, int nv, cudaStream_t st) {
   if (nv <= TPR) return forward_as<T, VEC, TPR, 1>(p, st);
