@@ -55,7 +55,9 @@ cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes) {
 }  // namespace svdq
 
 // Device error word: kernels OR ERR_* bits into it (one copy per device).
-__device__ unsigned g_svdq_error_word;
+// Zero from the module's load on: the first call may stand inside a stream
+// capture, where setting it through the legacy stream would end the capture.
+__device__ unsigned g_svdq_error_word = 0;
 
 struct svdq_weights {
   int dev;
@@ -135,7 +137,6 @@ svdq_status current_device(DevState** out) {
     if (sm100) {
       void* p = nullptr;
       if (cudaGetSymbolAddress(&p, g_svdq_error_word) != cudaSuccess) return from_cuda(cudaErrorUnknown);
-      if (cudaMemset(p, 0, sizeof(unsigned)) != cudaSuccess) return from_cuda(cudaErrorUnknown);
       d.err_word = static_cast<unsigned*>(p);
       if (!g_encode) {
         void* fn = nullptr;
