@@ -543,6 +543,10 @@ static bool elem_aligned(svdq_dtype dt, const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & (elem_bytes(dt) - 1)) == 0;
 }
 static bool float_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+// covers the row, under the 2^40 bytes that every 16-bit call takes: offsets stay far from 64 bits' end
+static bool row_stride_ok(svdq_dtype dt, long long ld, int C) {
+  return ld >= C && ld < (1ll << 40) / (long long)elem_bytes(dt);
+}
 static bool length_ok(int C) { return C >= 1 && C <= MOST; }
 static bool known_type(svdq_dtype dt) { return dt == SVDQ_BF16 || dt == SVDQ_FP16 || dt == SVDQ_FP32; }
 
@@ -551,7 +555,7 @@ svdq_status svdq_layernorm(svdq_dtype dt, int M, int C, const void* X, long long
                            cudaStream_t stream) {
   if (!known_type(dt) || !gamma != !beta || (M > 0 && (!X || !Y)) || !(eps >= 0.f) || !std::isfinite(eps))
     return SVDQ_ERR_INVALID_ARG;
-  if (!rows_ok(M) || !length_ok(C) || ldx < C || ldy < C) return SVDQ_ERR_SHAPE;
+  if (!rows_ok(M) || !length_ok(C) || !row_stride_ok(dt, ldx, C) || !row_stride_ok(dt, ldy, C)) return SVDQ_ERR_SHAPE;
   if (!elem_aligned(dt, X) || !elem_aligned(dt, gamma) || !elem_aligned(dt, beta) || !elem_aligned(dt, Y) ||
       !float_aligned(mean) || !float_aligned(rstd))
     return SVDQ_ERR_ALIGNMENT;
@@ -574,7 +578,9 @@ svdq_status svdq_layernorm_backward(svdq_dtype dt, int M, int C, const void* dY,
                                     long long lddx, void* dgamma, void* dbeta, void* workspace, size_t ws_bytes,
                                     cudaStream_t stream) {
   if (!known_type(dt) || !dgamma != !dbeta || (M > 0 && (!dY || !X || !mean || !rstd))) return SVDQ_ERR_INVALID_ARG;
-  if (!rows_ok(M) || !length_ok(C) || lddy < C || ldx < C || (dX && lddx < C)) return SVDQ_ERR_SHAPE;
+  if (!rows_ok(M) || !length_ok(C) || !row_stride_ok(dt, lddy, C) || !row_stride_ok(dt, ldx, C) ||
+      (dX && !row_stride_ok(dt, lddx, C)))
+    return SVDQ_ERR_SHAPE;
   if (!elem_aligned(dt, dY) || !elem_aligned(dt, X) || !elem_aligned(dt, gamma) || !elem_aligned(dt, dX) ||
       !elem_aligned(dt, dgamma) || !elem_aligned(dt, dbeta) || !float_aligned(mean) || !float_aligned(rstd) ||
       !aligned16(workspace))
