@@ -18,38 +18,27 @@
 #include "common.cuh"
 #include "dense.h"
 #include "kernels.h"
+#include "smem_table.h"
 
 using namespace svdq;
 
 namespace svdq {
 
-// (kernel, device) -> the dynamic shared-memory limit already set
+// Raises a kernel's dynamic shared-memory limit once a device (smem_table.h).
+// Up to 32 KB need no limit raised (48 KB a block without, the kernels' static
+// shared memory among them): such kernels are not looked up.
 cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes) {
-  struct Entry {
-    const void* fn;
-    int dev;
-    size_t bytes;
-  };
   static std::mutex mu;
-  static Entry table[256];
-  static int used = 0;
+  static SmemTable table;
+  if (bytes <= 32768) return cudaSuccess;
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(mu);
-  int i = 0;
-  for (; i < used; ++i)
-    if (table[i].fn == kernel && table[i].dev == dev) break;
-  if (i < used && table[i].bytes >= bytes) return cudaSuccess;
+  if (table.raised(kernel, dev) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e != cudaSuccess) return e;
-  if (i == used) {
-    if (used == 256) return cudaSuccess;   // table full: correct, only slower (set on every call)
-    table[used++] = Entry{kernel, dev, bytes};
-  } else {
-    table[i].bytes = bytes;
-  }
-  return cudaSuccess;
+  if (e == cudaSuccess) table.note(kernel, dev, bytes);
+  return e;
 }
 
 }  // namespace svdq
