@@ -223,6 +223,15 @@ __device__ __forceinline__ void fma_v(float* o, const float* a, const float* b, 
     }
 }
 
+// sum / c by one correction of sum * (1 / c), which alone is up to 1.5 steps
+// off: a row of one value has to have that value as its mean (1000 in 3584
+// columns was off by 6e-5, its output by 0.02).  A sum that is not finite is
+// its own mean.
+__device__ __forceinline__ float mean_of(float sum, float c, float inv_c) {
+  const float m = sum * inv_c, r = fmaf(fmaf(-m, c, sum), inv_c, m);
+  return r == r ? r : m;
+}
+
 // ------------------------------------------------------------------ sums over a row group
 // Sums over the tpr threads of a row group; every thread of the block calls
 // it.  `sh` alternates between two buffers, so one barrier a call is enough.
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(BLOCK_OF<TPR>, PER <= 4 ? 1024 / BLOCK_OF<TPR>
         add_to<VEC>(i & 1 ? acc2 : acc, x[i]);
       }
     acc = add2(acc, acc2);
-    const float mean = red.sum1(acc.x + acc.y) * inv_c;
+    const float mean = mean_of(red.sum1(acc.x + acc.y), (float)p.C, inv_c);
     if constexpr (RowRing::ON) {   // the slots have been read: the sum above needed their values
       fetch(row + DEPTH * stride, stage);
       stage = stage + 1 == DEPTH ? 0 : stage + 1;
@@ -442,7 +451,7 @@ __global__ void __launch_bounds__(MAX_TPR) layernorm_streamed_kernel(LayerNormPa
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s += f[j];
   }
-  const float mean = red.sum1(s) * inv_c;
+  const float mean = mean_of(red.sum1(s), (float)p.C, inv_c);
   s = 0.f;
   for (int c = threadIdx.x; c < nv; c += blockDim.x) {
     unpack<T, VEC>(x[c], f);
