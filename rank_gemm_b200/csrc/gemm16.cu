@@ -56,7 +56,9 @@
 // fixed parts: launch 1 us, first operands 1 to 2 us, an epilogue that nothing
 // overlaps 1 to 2.5 us.  Few rows: the weights' bytes (23 x 3072 -> 9216: 57
 // MB in 14.3 us, of which 9 us streaming) and the same fixed parts.
-// All waits are bounded (mbar_wait); TMEM is freed on every exit path.
+// All waits are bounded (mbar_wait).  When one runs out, the whole cluster
+// leaves together: after the loads, MMAs and partials that it has in flight (see
+// the end of the kernel), with TMEM freed.
 #include <type_traits>
 
 #include "common.cuh"
@@ -71,7 +73,7 @@ constexpr int SMEM_LIMIT = 232448;           // 227 KB
 constexpr int MAX_STAGES = 8;
 
 struct Ctl {
-  uint64_t full[MAX_STAGES], empty[MAX_STAGES], t_full[2], t_empty[2], inbox;
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES], t_full[2], t_empty[2], inbox, drain;
   uint32_t tmem_base;
   int abort;
 };
@@ -210,6 +212,18 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t 
       "r"(a), "r"(b), "r"(c), "r"(d), "r"(cluster_bar)
       : "memory");
 }
+// Tells the other CTAs of the cluster that a wait has run out.  Ordered before
+// this thread's next arrival on the cluster's barrier.
+__device__ __forceinline__ void tell_abort(uint32_t abort_word, int ctas) {
+  for (int r = 0; r < ctas; ++r)
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dsmem_map(abort_word, r)), "r"(1) : "memory");
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+// Waits for a phase on the way out: without a look at the abort flag, until `deadline`.
+__device__ __forceinline__ void wait_until(uint32_t bar, uint32_t parity, uint64_t deadline) {
+  while (!mbar_try_wait(bar, parity) && global_timer_ns() < deadline) {
+  }
+}
 // cluster_sync_all that orders no memory: an arrival with release semantics
 // would wait for this thread's stores to global memory.
 __device__ __forceinline__ void cluster_sync_last() {
@@ -330,6 +344,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
       mbar_init(smem_u32(&ctl->t_empty[s]), CG * C::EPI_WARPS);
     }
     mbar_init(smem_u32(&ctl->inbox), 1);
+    mbar_init(smem_u32(&ctl->drain), 1);
     ctl->abort = 0;
     fence_barrier_init();
     if (C::INBOX && S > 1) {   // the bytes the ranks will send: whole chunks of 16 columns up to the last token
@@ -398,6 +413,8 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
   auto k_begin = [&](const Gemm16Job& j, const Tile& t) { return k_at(j, t.part * S + split); };
   auto k_end = [&](const Gemm16Job& j, const Tile& t) { return k_at(j, t.part * S + split + 1); };
 
+  int load_stage = 0;          // producer: the first place in the ring that it has not filled,
+  uint32_t load_phase = 0;     // and that place's turn
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -450,6 +467,8 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
           }
         }
       }
+      load_stage = stage;
+      load_phase = phase;
       // the pair's commits have all arrived before this CTA may leave
       for (int i = 0; CG == 2 && ok && i < C::STAGES; ++i, next())
         ok = mbar_wait(smem_u32(&ctl->empty[stage]), phase ^ 1, abort_flag, p.err);
@@ -893,11 +912,47 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
     }
   }
 
+  if (*abort_flag && CG * S > 1) tell_abort(smem_u32(&ctl->abort), CG * S);
   tc_fence_before();
   if (CG * S > 1)
     cluster_sync_last();   // no CTA leaves while another reads its shared memory or signals its barriers
   else
     __syncthreads();
+  if (*abort_flag) {
+    // A wait has run out somewhere in the cluster (every thread of it sees the
+    // same here) and no thread issues anything any more.  What has been issued
+    // lands before a CTA leaves: loads on their stage's barrier, MMAs on one
+    // of their own, the other ranks' partials on the inbox.  A copy within the
+    // chip takes microseconds; a barrier that will never complete (some of its
+    // operations were not issued) is given up after 10 ms.
+    const uint64_t deadline = global_timer_ns() + 10000000ull;
+    if (warp == 0 && lane == 0) {
+      if (cta == 0) {
+        for (int s = 0; s < C::STAGES; ++s)
+          wait_until(smem_u32(&ctl->full[s]), s < load_stage ? load_phase : load_phase ^ 1, deadline);
+      } else {   // its loads count on the other CTA's barriers, which may not expect them: 1 ms
+        while (global_timer_ns() + 9000000ull < deadline) {
+        }
+      }
+    }
+    if (warp == 1 && cta == 0) {
+      __syncwarp();
+      if (elect_one()) {   // the lane that issued the MMAs
+        if (CG == 2)
+          tc_commit_pair(smem_u32(&ctl->drain), (uint16_t)(1u << rank));
+        else
+          tc_commit(smem_u32(&ctl->drain));
+        wait_until(smem_u32(&ctl->drain), 0, deadline);
+      }
+      __syncwarp();
+    }
+    if (C::INBOX && S > 1 && warp == 2 && lane == 0) wait_until(smem_u32(&ctl->inbox), 0, deadline);
+    tc_fence_before();
+    if (CG * S > 1)
+      cluster_sync_all();
+    else
+      __syncthreads();
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
