@@ -415,6 +415,12 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
 
   int load_stage = 0;          // producer: the first place in the ring that it has not filled,
   uint32_t load_phase = 0;     // and that place's turn
+  // The waits that last for a whole reduction have a limit that grows with it:
+  // the set one besides for every 65536 k-tiles (30 us a k-tile at 2 s).
+  auto reduction_err = [&](const Gemm16Job& j) {
+    return DeviceErr{p.err.word, p.err.limit_ns + (p.err.limit_ns >> 16) * (unsigned)j.nk};
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -670,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
         }
       };
       uint4 res[2] = {residual8(m, n_tile + c0), residual8(m, n_tile + c0 + 8)};
-      if (!mbar_wait(smem_u32(&ctl->t_full[ab]), pt, abort_flag, p.err)) break;
+      if (!mbar_wait(smem_u32(&ctl->t_full[ab]), pt, abort_flag, reduction_err(j))) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16) + ab * (TALL ? BN : C::ACC_COLS);
       const bool second = GRAD && t.second;
@@ -804,7 +810,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
       if (!t.valid) break;
       const uint32_t ab = n & 1, pt = (n >> 1) & 1;
       // the four warps leave together when the wait runs out: emit_tokens joins them
-      const bool ok = mbar_wait(smem_u32(&ctl->t_full[ab]), pt, abort_flag, p.err);
+      const bool ok = mbar_wait(smem_u32(&ctl->t_full[ab]), pt, abort_flag, reduction_err(p.job[0]));
       if (!all_warps_ok(ok)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16) + ab * C::ACC_COLS;
@@ -837,7 +843,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
     const Gemm16Job& j = p.job[t.job];
     bool ok = false;
     if (warp >= 2) {
-      ok = mbar_wait(smem_u32(&ctl->t_full[0]), 0, abort_flag, p.err);
+      ok = mbar_wait(smem_u32(&ctl->t_full[0]), 0, abort_flag, reduction_err(j));
       tc_fence_after();
     }
     if (!C::INBOX) cluster_sync_all();
@@ -865,7 +871,7 @@ __global__ void __launch_bounds__(Cfg<CG, BN, SWAP, GATED, TALL>::THREADS, 1)
     if (!C::INBOX)
       cluster_sync_all();
     else if (warp >= 2)
-      ok = mbar_wait(smem_u32(&ctl->inbox), 0, abort_flag, p.err) && ok;
+      ok = mbar_wait(smem_u32(&ctl->inbox), 0, abort_flag, reduction_err(j)) && ok;
     // columns col .. col + 3 of the half
     auto total4 = [&](int half, int col, float* v) {
       const uint32_t from = inbox + half * 128 * line + col * 4;

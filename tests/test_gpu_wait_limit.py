@@ -3,7 +3,10 @@ reads SVDQ_WAIT_LIMIT_MS once a process, so each case is a process of its own,
 spawned) a product whose single tile takes several milliseconds gives up. The
 call's kernel then ends by itself, svdq_poll_device_error reports a timeout,
 and the next call in the same process is right: the cluster left only after
-what it had in flight had landed, and gave its tensor memory back."""
+what it had in flight had landed, and gave its tensor memory back.
+
+The limit of a wait for a whole reduction grows with the reduction, so that a
+long one is not taken for a stuck one: sizes up to 2^31 - 512 are allowed."""
 import multiprocessing as mp
 import os
 
@@ -86,3 +89,31 @@ def run_child(target, args, limit_ms):
 @pytest.mark.parametrize("form", ["swapped, split", "gated, swapped", "pair, split", "backward"])
 def test_a_product_that_runs_out_of_time(form):
     assert run_child(_child, (form,), 1) == ([7, 7, 0], [True, True])
+
+
+def _long_reduction(gated, queue):
+    """2^21 k-tiles over 4 ranks (at least 150 cycles each: 40 ms and more,
+    twice the limit of 20 ms), zero but for a few products that are exact."""
+    try:
+        from rank_gemm_b200 import binding as B
+        K = 1 << 27
+        X, W = torch.zeros(1, K, dtype=BF, device="cuda"), torch.zeros(8, K, dtype=BF, device="cuda")
+        at = torch.tensor([0, 63, K // 4, K // 2 + 77, K - 1], device="cuda")
+        X[0, at] = torch.tensor([1.0, 2.0, 3.0, 4.0, 5.0], device="cuda").to(BF)
+        W[:, at] = torch.arange(40, device="cuda").reshape(8, 5).to(BF)
+        want = X[:, at].float() @ W[:, at].float().T
+        Y = torch.full((1, 8), float("nan"), dtype=BF, device="cuda")
+        if gated:      # act none: the product of the two sums
+            B.svdq_gated_linear(1, K, 8, X, W, W, None, None, 0, Y)
+            want = want * want
+        else:
+            B.svdq_dense_linear(1, K, 8, X, W, None, 0, None, Y)
+        status = B.svdq_poll_device_error()
+        queue.put((status, bool(torch.equal(Y, want.to(BF)))))
+    except BaseException as e:  # noqa: BLE001  (reported by the parent)
+        queue.put("%s: %s" % (type(e).__name__, str(e)[:300]))
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_a_long_reduction_is_not_taken_for_a_stuck_one(gated):
+    assert run_child(_long_reduction, (gated,), 20) == (0, True)
