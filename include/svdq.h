@@ -614,6 +614,14 @@ const char* svdq_status_string(svdq_status s);
  * capability check (major < 0 restores the real value). */
 void svdq_debug_override_cc(int major, int minor);
 
+/* Test hook: the tiling that the 16-bit products of a call take on a device of
+ * num_sms SMs (nothing is launched; no GPU is needed).  op 0 svdq_dense_linear,
+ * 1 svdq_gated_linear, 2 and 3 their backward passes with dX and the weights'
+ * gradients; N the output features (F).  plan [6]: swapped form, MMA columns,
+ * CTAs (pairs) a reduction is split over, 512-row tiles, and the parts that
+ * dX's and the weight gradient's reductions are cut into. */
+svdq_status svdq_debug_product_plan(int op, int M, int K, int N, int num_sms, int* plan);
+
 #ifdef __cplusplus
 }
 #endif

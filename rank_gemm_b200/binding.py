@@ -107,6 +107,7 @@ _SIGS = {
     "svdq_poll_device_error": (_i, [_vp]),
     "svdq_selftest_wait_timeout": (_i, [ctypes.c_uint, _vp]),
     "svdq_debug_override_cc": (None, [_i, _i]),
+    "svdq_debug_product_plan": (_i, [_i, _i, _i, _i, _i, ctypes.POINTER(_i)]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -478,3 +479,10 @@ def svdq_selftest_wait_timeout(limit_us, stream=None):
 
 def svdq_debug_override_cc(major, minor):
     lib.svdq_debug_override_cc(major, minor)
+
+
+def svdq_debug_product_plan(op, M, K, N, num_sms=148):
+    """(swapped form, MMA columns, ranks, tall tiles, parts of dX, parts of the weight gradient)"""
+    plan = (_i * 6)()
+    _check(lib.svdq_debug_product_plan(op, M, K, N, num_sms, plan), "svdq_debug_product_plan")
+    return tuple(plan)

@@ -165,6 +165,13 @@ constexpr int SWAP_ROWS = 256;
 // empty, come slower than full ones (gated 2 x 1272 -> 4344: 12.7 us, swapped 9.1).
 constexpr int PAIR_ROWS = 32;
 
+// The tiling of a forward product of M rows, N (two weights: of each) features.
+Gemm16Plan plan_forward(Gemm16Op op, int M, int N, int nk, int num_sms) {
+  const Choice pair = plan_pair(op, {M, N, nk, 1, 1}, {}, num_sms);
+  const Choice swapped = M <= SWAP_ROWS ? plan_swap(op, M, N, nk, num_sms) : Choice{};
+  return M <= PAIR_ROWS || (swapped.cycles > 0 && swapped.cycles < pair.cycles) ? swapped.plan : pair.plan;
+}
+
 // ------------------------------------------------------------------ operands
 struct Operand {
   const void* ptr;
@@ -225,18 +232,14 @@ svdq_status forward_product(const DeviceInfo& d, svdq_dtype dt, int M, int K, in
   j.parts = 1;
   j.Y = out16(Y);
   j.ldy = ldy;
-  Gemm16Plan plan;
+  const Gemm16Plan plan = plan_forward(op, M, N, nk, d.num_sms);
   Gemm16Maps<2> maps;
   bool ok;
-  const Choice pair = plan_pair(op, {M, N, nk, 1, 1}, {}, d.num_sms);
-  const Choice swapped = M <= SWAP_ROWS ? plan_swap(op, M, N, nk, d.num_sms) : Choice{};
-  if (M <= PAIR_ROWS || (swapped.cycles > 0 && swapped.cycles < pair.cycles)) {
-    plan = swapped.plan;
+  if (plan.swap) {
     j.tiles_m = ceil_div(N, 128);
     j.tiles_n = ceil_div(M, plan.bn);
     ok = encode_job(plan, dt, w, W2 ? &w2 : nullptr, x, nullptr, j, p.Z, p.Z2, maps.m[0]);
   } else {
-    plan = pair.plan;
     j.tiles_m = ceil_div(M, plan.tall ? 512 : 256);
     j.tiles_n = ceil_div(N, W2 ? plan.bn / 2 : plan.bn);
     ok = encode_job(plan, dt, x, nullptr, w, W2 ? &w2 : nullptr, j, p.Z, p.Z2, maps.m[0]);
@@ -271,6 +274,31 @@ size_t partials_bytes(int M, int K, int N, bool two) {
   return b.dx + b.dw;
 }
 
+// The products of a backward pass: the gradients asked for as jobs, the one of
+// the longer tiles first, and their tiling.
+struct BackwardPlan {
+  int jobs = 0, at_w = -1, at_x = -1;   // of which number
+  JobShape shape[2] = {};
+  Choice choice;
+};
+BackwardPlan plan_backward(int M, int K, int N, bool two, bool dW, bool dX, int num_sms) {
+  BackwardPlan b;
+  const int nk_w = ceil_div(M, 64), nk_x = ceil_div(N, 64) * (two ? 2 : 1);
+  const bool x_first = dX && (!dW || nk_x > nk_w);
+  if (dW) {
+    b.at_w = x_first ? 1 : 0;
+    b.shape[b.at_w] = {N, K, nk_w, two ? 2 : 1, most_parts(part_rows(N, two ? 2 : 1), K, nk_w)};
+    ++b.jobs;
+  }
+  if (dX) {
+    b.at_x = dW && !x_first ? 1 : 0;
+    b.shape[b.at_x] = {M, K, nk_x, 1, most_parts(part_rows(M, 1), K, nk_x)};
+    ++b.jobs;
+  }
+  if (b.jobs) b.choice = plan_pair(GEMM16_GRAD, b.shape[0], b.shape[1], num_sms);
+  return b;
+}
+
 // The products of a backward pass, dZ (and dZ2) [M][N] of row stride ldz:
 //   dW [N][K] = dZ^T X, dW2 = dZ2^T X (stacked below it)   when dW
 //   dX [M][K] = dZ W + dZ2 W2                              when dX
@@ -288,51 +316,36 @@ svdq_status backward_products(const DeviceInfo& d, svdq_dtype dt, const Backward
   const Operand z{g.dZ, N, M, ldz}, z2{g.dZ2, N, M, ldz}, w{g.W, K, N, K}, w2{g.W2, K, N, K},
       x{g.X, K, M, (uint64_t)g.ldx};
   const bool two = g.dZ2 != nullptr;
-  int jobs = 0, at_w = -1, at_x = -1;
-  JobShape shape[2] = {};
-  if (g.dW) {
-    at_w = jobs++;
+  const BackwardPlan b = plan_backward(g.M, g.K, g.N, two, g.dW, g.dX, d.num_sms);
+  const int jobs = b.jobs, at_w = b.at_w, at_x = b.at_x;
+  if (!jobs) return SVDQ_OK;
+  if (at_w >= 0) {
     Gemm16Job& j = p.job[at_w];
     j.M = g.N;
     j.N = g.K;
-    j.nk1 = j.nk = ceil_div(g.M, 64);
+    j.nk1 = j.nk = b.shape[at_w].nk;
     j.a_mn = 1;
     j.Y = out16(g.dW);
     j.Y2 = out16(g.dW2);
     j.ldy = g.K;
     j.P = reinterpret_cast<float*>(g.partials + part_bytes(g.M, g.K, g.N, two).dx);
-    shape[at_w] = {g.N, g.K, j.nk, two ? 2 : 1, most_parts(part_rows(g.N, two ? 2 : 1), g.K, j.nk)};
   }
-  if (g.dX) {
-    at_x = jobs++;
+  if (at_x >= 0) {
     Gemm16Job& j = p.job[at_x];
     j.M = g.M;
     j.N = g.K;
     j.nk1 = ceil_div(g.N, 64);
-    j.nk = two ? 2 * j.nk1 : j.nk1;
+    j.nk = b.shape[at_x].nk;
     j.Y = out16(g.dX);
     j.ldy = g.lddx;
     j.P = reinterpret_cast<float*>(g.partials);
-    shape[at_x] = {g.M, g.K, j.nk, 1, most_parts(part_rows(g.M, 1), g.K, j.nk)};
   }
-  if (!jobs) return SVDQ_OK;
-  if (jobs == 2 && p.job[1].nk > p.job[0].nk) {   // the longer tiles first
-    const Gemm16Job t = p.job[0];
-    p.job[0] = p.job[1];
-    p.job[1] = t;
-    const JobShape u = shape[0];
-    shape[0] = shape[1];
-    shape[1] = u;
-    at_w ^= 1;
-    at_x ^= 1;
-  }
-  const Choice choice = plan_pair(GEMM16_GRAD, shape[0], shape[1], d.num_sms);
-  const Gemm16Plan& plan = choice.plan;
+  const Gemm16Plan& plan = b.choice.plan;
   for (int i = 0; i < jobs; ++i) {
     p.job[i].tiles_n = ceil_div(g.K, plan.bn);
-    p.job[i].tiles_m1 = ceil_div(shape[i].M, plan.tall ? 512 : 256);
-    p.job[i].tiles_m = shape[i].stacked * p.job[i].tiles_m1;
-    p.job[i].parts = choice.parts[i];
+    p.job[i].tiles_m1 = ceil_div(b.shape[i].M, plan.tall ? 512 : 256);
+    p.job[i].tiles_m = b.shape[i].stacked * p.job[i].tiles_m1;
+    p.job[i].parts = b.choice.parts[i];
   }
   Gemm16Maps<2> maps;
   if (at_w >= 0 &&
@@ -360,6 +373,25 @@ cudaError_t zero(void* p, size_t bytes, cudaStream_t stream) {
 }  // namespace
 
 extern "C" {
+
+// ------------------------------------------------------------------ how products are tiled (test hook)
+svdq_status svdq_debug_product_plan(int op, int M, int K, int N, int num_sms, int* plan) {
+  if (op < 0 || op > 3 || !plan || num_sms < 8) return SVDQ_ERR_INVALID_ARG;
+  if (!rows_ok(M) || M == 0 || !width_ok(K) || !width_ok(N)) return SVDQ_ERR_SHAPE;
+  Gemm16Plan g;
+  int parts_x = 1, parts_w = 1;
+  if (op < 2) {
+    g = plan_forward(op ? GEMM16_GATED : GEMM16_NT, M, N, ceil_div(K, 64), num_sms);
+  } else {
+    const BackwardPlan b = plan_backward(M, K, N, op == 3, true, true, num_sms);
+    g = b.choice.plan;
+    parts_x = b.choice.parts[b.at_x];
+    parts_w = b.choice.parts[b.at_w];
+  }
+  const int out[6] = {g.swap, g.bn, g.splits, g.tall, parts_x, parts_w};
+  std::copy(out, out + 6, plan);
+  return SVDQ_OK;
+}
 
 // ------------------------------------------------------------------ dense linear
 svdq_status svdq_dense_linear(svdq_dtype dt, int M, int K, int N, const void* X, long long ldx, const void* W_t,
