@@ -512,7 +512,12 @@ svdq_status svdq_awq_gemm(const svdq_awq_weights* w, int M, const void* X, void*
  *   - dt: SVDQ_BF16 or SVDQ_FP16 (layer norm: also SVDQ_FP32); every tensor
  *     of a call has that type except mean and rstd (float32).  Sums are
  *     float32; every output is rounded once from float32.  A backward pass
- *     also rounds dZ (dG, dU) to dt, the operand type of its products.
+ *     also rounds dZ (dG, dU) to dt, the operand type of its products: dX and
+ *     the weight gradients are then about 1.4 times as far from exact as
+ *     with a dZ in float32, and in fp16 they have dZ's range: a dZ (dH u
+ *     act'(g), dH act(g)) above 65504 is infinite, one below 2^-25 is zero,
+ *     whatever the product would have been.  The bias gradients sum the
+ *     float32 values.
  *   - Activations (X, Y, residual, H, dY, dH, dX) are rows with a stride ld in
  *     elements, ld >= the row's length, ld % 8 == 0 (layer norm: any).
  *     Weights, biases, kept pre-activations (Z, G, U) and weight gradients are

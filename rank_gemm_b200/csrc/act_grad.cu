@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(THREADS) act_grad_kernel(ActGradParams p) {
 }
 
 // 32 columns x 32 part lanes a block: lane l adds parts l, l + 32, ..., then
-// the lanes in order.
+// the lanes as a tree, the same one every time.
 constexpr int SUM_LANES = 32;
 __global__ void __launch_bounds__(32 * SUM_LANES) sum_parts_kernel(const float* part, const float* part2, int parts,
                                                                    int N, int dt, void* out, void* out2) {
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(32 * SUM_LANES) sum_parts_kernel(const float* 
 
 // Row ranges: as many blocks as the SMs hold at four each and no more (a
 // second, nearly empty round cost 148 us instead of 103 for 4608 x 12288
-// gated), at least 16 rows each.
+// gated), and no more than one for every 16 rows (8 to 16 rows each then).
 int act_grad_parts(int M, int N) {
   const int cb = (int)(((long long)N + COLS - 1) / COLS);
   int parts = 148 * 4 / cb;

@@ -45,8 +45,15 @@ int clusters(int width, int num_sms) {
 // k-tile by k-tile, or, where that is longer, the time the operand bytes take
 // from L2 (8500 a cycle over the chip) or the weights from memory (3400);
 // besides, a fixed part (launch, fill, epilogue, drain) and the exchange of a
-// split tile's partials.  The constants fit 24 shapes (1 .. 2048 rows, 1024 x
-// 1024 .. 12288 x 3072, one and two weights) under every tiling.  Where the
+// split tile's partials.  The constants were fitted to 24 shapes of 1 to 2048
+// rows under every tiling.  Of 120 shapes drawn at random, all four operators,
+// 112 took at most 1.08 times their best tiling's time; the others, us chosen
+// and best: 179 x 8216 -> 6776 46.3, 36.9 (256 columns split in two); gated 1 x
+// 12056 -> 104 21.0, 17.1 (pair form split in four); gated backward 6 x 5080 ->
+// 11136 156, 135 (not cut); gated 1004 x 1160 -> 1440 15.7, 13.8 and 1580 x 776
+// -> 1064 16.3, 15.0 (256 columns); backward 66 x 224 -> 11848 15.0, 13.4 and 77
+// x 296 -> 1296 9.3, 8.5 (128 columns, cut); 1319 x 5720 -> 824 31.4, 28.5.  A
+// pair's rate for weights from memory is not in the estimate.  Where the
 // two forms cross (us, best tilings of each): 64 x 1024 -> 1024 swapped 4.9,
 // pair 6.4; 128 x 12288 -> 3072 swapped 24.4, pair 26.7; 128 x 3072 -> 9216
 // swapped 15.8, pair 15.6; 256 x 1024 -> 1024 swapped 8.6, pair 6.6.
@@ -161,8 +168,11 @@ Choice plan_swap(Gemm16Op op, int tokens, int features, int nk, int num_sms) {
 }
 // More rows of X than this never gain from the swapped form.
 constexpr int SWAP_ROWS = 256;
-// Up to this many rows the pair form never gains: its 256-row boxes, nearly
-// empty, come slower than full ones (gated 2 x 1272 -> 4344: 12.7 us, swapped 9.1).
+// Up to this many rows the pair form is not taken: its 256-row boxes, nearly
+// empty, come slower than full ones, which its estimate does not know (gated 2 x
+// 1272 -> 4344: 12.7 us, swapped 9.1).  It would gain where a long reduction
+// has few features, whose weights the swapped form streams through at most 4
+// CTAs a tile for one token (gated 1 x 12056 -> 104: 17.1 us, swapped 21.0).
 constexpr int PAIR_ROWS = 32;
 
 // The tiling of a forward product of M rows, N (two weights: of each) features.
